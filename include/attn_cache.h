@@ -1,0 +1,181 @@
+/*
+ * attn_cache.h -- C ABI of the paged key/value cache of the B200 (sm_100a)
+ * attention library: appending a step's keys and values to it, and attention
+ * over it.
+ *
+ * The cache is a pool of pages.  A page holds page_size consecutive tokens of
+ * one sequence; row b of page_table lists the pages of sequence b in order, so
+ * key j of sequence b is slot j % page_size of page
+ * page_table[b][j / page_size].  The pool holds BF16, or E4M3 with one FP32
+ * scale for each page and key/value head (the stored byte stands for
+ * scale * value), for keys and for values.
+ *
+ * A serving step of n new tokens per sequence is attn_cache_append, then
+ * attn_fwd_cache, with the same page_table, seqlens_k and cu_seqlens.
+ *
+ * Status codes, the device rule and the bounded waits are those of
+ * attn_fwd.h.  Arguments are validated before any CUDA call; on an error
+ * nothing is written.  Both calls are asynchronous on `stream`, allocate
+ * nothing, keep nothing between calls and can be captured into a graph.
+ * Page numbers outside 0 .. num_pages - 1 are never followed: such keys are
+ * not written by attn_cache_append, and count as zeros in attn_fwd_cache.
+ */
+#ifndef SDPA10_ATTN_CACHE_H
+#define SDPA10_ATTN_CACHE_H
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "attn_fwd.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef enum {
+    ATTN_CACHE_BF16 = 0,
+    ATTN_CACHE_E4M3 = 1
+} attn_cache_type_t;
+
+/*
+ * The pool.  Element (page, token, head, i) of keys and of values is at
+ * page * page_stride + token * token_stride + head * head_stride + i
+ * (elements), so [num_pages, page_size, h_kv, 128] and [num_pages, h_kv,
+ * page_size, 128] are both described.
+ *
+ *   k_pages, v_pages   device, 16-byte aligned
+ *   k_scale, v_scale   device, fp32 [num_pages, h_kv] contiguous (E4M3 only;
+ *                      must be null for BF16).  0 marks a page whose values
+ *                      are all zero.  v_scale must be below 2^64, and values
+ *                      under a v_scale below 2^-64 count as zeros
+ *   strides            positive, multiples of 16 bytes, below 2^40 bytes
+ *   page_size          a multiple of 8
+ *   d                  must be 128
+ */
+typedef struct {
+    void* k_pages;
+    void* v_pages;
+    float* k_scale;
+    float* v_scale;
+    int64_t page_stride;
+    int64_t token_stride;
+    int64_t head_stride;
+    int num_pages;
+    int page_size;
+    int h_kv;
+    int d;
+    int type; /* attn_cache_type_t */
+} attn_cache_t;
+
+/*
+ * attn_cache_append -- write the keys and values of a step's new tokens into
+ * the pages of their sequences, the keys rotated by their positions, and
+ * rotate the step's queries.
+ *
+ *   k, v   device, bf16 [total, h_kv, 128] (read), q the same with h_q heads
+ *          or null (no queries: q_out is then null too)
+ *   q_out  device, bf16 [total, h_q, 128] contiguous (written); may not
+ *          overlap the inputs
+ *   k_stride, v_stride, q_stride   elements from one token to the next
+ *          (multiples of 8; a token's heads are contiguous, so slices of one
+ *          fused projection can be given)
+ *   page_table   device, int32 [batch, max_pages] contiguous
+ *   seqlens_k    device, int32 [batch]: each sequence's keys, the new ones
+ *                included
+ *   cu_seqlens   device, int32 [batch + 1], non-decreasing from 0: sequence b
+ *                brings rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1.  Null:
+ *                total / batch rows each (total must be a multiple of batch).
+ *                Rows from cu_seqlens[batch] on are padding: not read, and
+ *                q_out is left as it was there
+ *   max_seqlen   upper bound of the sequences' new rows; rows past it are
+ *                not processed
+ *   inv_freq     device, fp32 [rotary_dim / 2] (null iff rotary_dim is 0)
+ *   rotary_dim   0 .. 128, a multiple of 16: the first rotary_dim elements of
+ *                a head are rotated, the others pass unchanged
+ *   interleaved  0: element i pairs with i + rotary_dim / 2; 1: element 2i
+ *                pairs with 2i + 1
+ *
+ * The i-th of a sequence's n new rows has position p = seqlens_k - n + i.
+ * Its pair f, (x, y), becomes
+ *     (x cos(p inv_freq[f]) - y sin(p inv_freq[f]),
+ *      y cos(p inv_freq[f]) + x sin(p inv_freq[f])),
+ * the angle taken in FP64 (far positions keep their phase), the product in
+ * FP32.  Rows at a negative position, or past max_pages * page_size, are not
+ * written to the cache; their queries are rotated all the same.
+ *
+ * E4M3: for every page and head that receives rows, scale = the smallest power
+ * of two s with bound <= 448 s, where bound is the largest |x| + |y| of the
+ * new rows' rotated pairs (no rotation of the pair exceeds it, so the scale
+ * depends neither on positions nor on how sines are rounded) and |x| of the
+ * elements that are not rotated; a page entered at its slot 0 starts afresh,
+ * any other keeps max(old scale, s), and where that grows the tokens already
+ * in the page are coded again under the new scale (exact but for values that
+ * become subnormal).  Values are rounded once from FP32 to E4M3.  Two rows of
+ * one call must not name the same slot, and no other sequence may hold a page
+ * that the call writes.
+ *
+ * One launch.  Errors: ATTN_ERR_INVALID (null pointers, sizes <= 0,
+ * h_q % h_kv, rotary_dim or strides out of range, page_size not a multiple of
+ * 8), ATTN_ERR_UNSUPPORTED (d != 128), ATTN_ERR_ALIGN (a tensor not 16-byte
+ * aligned, an int32 or fp32 array not 4-byte aligned), ATTN_ERR_CUDA.
+ */
+int attn_cache_append(const attn_cache_t* cache, const void* k, const void* v, const void* q,
+                      void* q_out, const int* page_table, const int* seqlens_k,
+                      const int* cu_seqlens, const float* inv_freq, int batch, int max_pages,
+                      int total, int max_seqlen, int h_q, int64_t k_stride, int64_t v_stride,
+                      int64_t q_stride, int rotary_dim, int interleaved, void* stream);
+
+/*
+ * attn_fwd_cache -- attention of a packed batch of queries over the pages of
+ * their sequences: for query i of a sequence's n, with its length
+ * L = seqlens_k[b],
+ *     S_j = scale * q . K_j,  O = sum_j softmax(S)_j V_j,
+ *     LSE = log sum_j exp(S_j)
+ * over the keys j of the sequence that it sees: all j < L, with causal = 1
+ * those with j <= L - n + i (the new tokens are the last ones), and with a
+ * window those of them with j >= L - n + i - window_left.
+ *
+ *   q     device, bf16 [total_q, h_q, 128] (read), q_stride elements from one
+ *         token to the next (a multiple of 8), 16-byte aligned
+ *   o     device, bf16 [total_q, h_q, 128] contiguous (written)
+ *   lse   device, fp32 [h_q, total_q] contiguous (written)
+ *   page_table, seqlens_k, cu_seqlens_q, max_seqlen_q   as attn_cache_append;
+ *         rows from cu_seqlens_q[batch] on are padding: their o and lse are
+ *         left as they were
+ *   window_left  -1: none; >= 0 needs causal = 1
+ *   scale        any finite value
+ *   workspace    device, at least attn_fwd_cache_workspace_bytes(...) bytes,
+ *                256-byte aligned; nothing in it needs to be set before a
+ *                call, and calls that may run at the same time need one each
+ *
+ * A row that sees no key (a sequence of length 0, or a causal one with more
+ * new rows than keys) gets O = 0 and LSE = -inf.  What lies in a page past the
+ * sequence's end is never used, whatever its bits.  Keys past
+ * max_pages * page_size are not there.
+ *
+ * Numerics: BF16 pages as attn_fwd (P rounded to BF16).  E4M3 pages go to the
+ * tensor core as they are; a query is the sum of two E4M3 numbers (exact for
+ * elements within 2^-9 of its largest, the others within 2^-18 of that) and a
+ * weight P the sum of three E5M2 numbers (9 bits, from the largest down to
+ * 2^-23 of it), so neither loses what BF16 operands would keep.  Sums are
+ * FP32.
+ *
+ * Two launches.  Errors as attn_cache_append, plus ATTN_ERR_INVALID for a
+ * non-finite scale, a window without causal and a workspace too small.
+ */
+int attn_fwd_cache(const attn_cache_t* cache, const void* q, void* o, float* lse,
+                   const int* page_table, const int* seqlens_k, const int* cu_seqlens_q,
+                   int batch, int max_pages, int total_q, int max_seqlen_q, int h_q,
+                   int64_t q_stride, int causal, int window_left, float scale, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* Device workspace bytes that attn_fwd_cache needs on the current device (0
+ * on bad sizes or without a device).  It grows with h_q / h_kv * max_seqlen_q
+ * up to 64 rows and not beyond. */
+size_t attn_fwd_cache_workspace_bytes(int h_q, int h_kv, int max_seqlen_q);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SDPA10_ATTN_CACHE_H */

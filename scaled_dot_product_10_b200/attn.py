@@ -1,4 +1,5 @@
-"""ctypes binding of the C ABI in ``include/attn_fwd.h``.
+"""ctypes binding of the C ABI in ``include/attn_fwd.h``, ``include/attn_bwd.h``
+and ``include/attn_cache.h``.
 
 Argument marshalling only: every step of the forward runs in the CUDA
 library.  Loading fails loudly if the library is missing -- there is no
@@ -26,6 +27,7 @@ _lib = None
 # (name, restype, argtypes) of every exported entry point.
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 _SIGNATURES = [
     ("attn_fwd", _I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P]),
     ("attn_fwd_window", _I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P]),
@@ -50,6 +52,11 @@ _SIGNATURES = [
     ("attn_merge_partials", _I, [_P, _P, _I, _I, _I, _I, _I, _P, _P, _P]),
     ("attn_fwd_partials", _I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float,
                                _P]),
+    ("attn_cache_append", _I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _L, _L, _L,
+                               _I, _I, _P]),
+    ("attn_fwd_cache", _I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _L, _I, _I,
+                            ctypes.c_float, _P, ctypes.c_size_t, _P]),
+    ("attn_fwd_cache_workspace_bytes", ctypes.c_size_t, [_I, _I, _I]),
     ("attn_status", _I, [_P]),
     ("attn_strerror", ctypes.c_char_p, [_I]),
     ("attn_set_wait_timeout_ns", _I, [ctypes.c_uint64]),
@@ -458,6 +465,204 @@ def merge_partials(o_parts, lse_parts, o=None, lse=None, stream=None):
                                                 _stream_handle(stream))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_merge_partials")
+    return o, lse
+
+
+class _CacheStruct(ctypes.Structure):
+    """attn_cache_t of include/attn_cache.h."""
+    _fields_ = [("k_pages", _P), ("v_pages", _P), ("k_scale", _P), ("v_scale", _P),
+                ("page_stride", _L), ("token_stride", _L), ("head_stride", _L),
+                ("num_pages", _I), ("page_size", _I), ("h_kv", _I), ("d", _I), ("type", _I)]
+
+
+class KVCache:
+    """A pool of cache pages for :func:`attn_cache_append` and
+    :func:`attn_fwd_cache`, checked once and kept from step to step.
+
+    ``k_pages`` and ``v_pages``: CUDA [num_pages, page_size, h_kv, 128],
+    BF16, or float8_e4m3fn with ``k_scale`` and ``v_scale`` FP32
+    [num_pages, h_kv] (the stored value times its page's and head's scale is
+    the value meant).  Any strides that both share and whose last is 1, so a
+    permuted [num_pages, h_kv, page_size, 128] or a slice of a larger pool
+    will do.  The page size is a multiple of 8.  The handle keeps the tensors
+    alive; what it points to is the tensors' memory at the time it was made.
+    """
+
+    def __init__(self, k_pages, v_pages, k_scale=None, v_scale=None):
+        import torch
+        e4m3 = k_pages.dtype == torch.float8_e4m3fn
+        for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+            if t.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or t.dtype != k_pages.dtype:
+                raise TypeError(f"{name} must be bfloat16 or float8_e4m3fn, both pools the same")
+            if t.dim() != 4 or t.shape[3] != 128 or t.stride(3) != 1 or 0 in t.shape:
+                raise ValueError(f"{name} must be [num_pages, page_size, heads, 128], "
+                                 "the last contiguous")
+        if k_pages.shape != v_pages.shape:
+            raise ValueError("k_pages and v_pages shapes disagree")
+        # A dimension of size 1 has no stride to speak of.
+        strides = [[t.stride(i) if t.shape[i] > 1 else 128 for i in range(3)]
+                   for t in (k_pages, v_pages)]
+        if strides[0] != strides[1]:
+            raise ValueError("k_pages and v_pages must have the same strides")
+        num_pages, page_size, h_kv, d = k_pages.shape
+        tensors = dict(k_pages=k_pages, v_pages=v_pages)
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if e4m3 != (t is not None):
+                raise ValueError("float8_e4m3fn pages need k_scale and v_scale, bfloat16 pages "
+                                 "take none")
+            if t is not None:
+                tensors[name] = t
+        self.device = _cuda_device(None, **tensors)
+        if e4m3:
+            for name in ("k_scale", "v_scale"):
+                _check_out(tensors[name], name, (num_pages, h_kv), torch.float32, self.device)
+        self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
+        self.num_pages, self.page_size, self.h_kv = num_pages, page_size, h_kv
+        self._struct = _CacheStruct(k_pages.data_ptr(), v_pages.data_ptr(),
+                                    k_scale.data_ptr() if e4m3 else None,
+                                    v_scale.data_ptr() if e4m3 else None, *strides[0], num_pages,
+                                    page_size, h_kv, d, int(e4m3))
+        self._ref = ctypes.addressof(self._struct)
+
+
+def _packed_rows(name, t, heads=None):
+    """Checks a [tokens, heads, 128] BF16 tensor whose heads are contiguous
+    within a token; returns its token stride."""
+    import torch
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16")
+    if t.dim() != 3 or t.shape[2] != 128 or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, 128]")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != 128):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * 128
+
+
+def _cache_batch(cache, page_table, seqlens_k, cu, cu_name):
+    """Checks a step's int32 tensors; returns (batch, max_pages)."""
+    import torch
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_contiguous():
+        raise ValueError("page_table must be a contiguous int32 [batch, max_pages]")
+    batch, max_pages = page_table.shape
+    if seqlens_k.dtype != torch.int32 or tuple(seqlens_k.shape) != (batch,) \
+            or not seqlens_k.is_contiguous():
+        raise ValueError("seqlens_k must be a contiguous int32 [batch]")
+    if cu is not None and (cu.dtype != torch.int32 or tuple(cu.shape) != (batch + 1,)
+                           or not cu.is_contiguous()):
+        raise ValueError(f"{cu_name} must be a contiguous int32 [batch + 1]")
+    return batch, max_pages
+
+
+def attn_cache_append(cache: KVCache, k, v, page_table, seqlens_k, cu_seqlens=None,
+                      max_seqlen: int | None = None, q=None, q_out=None, inv_freq=None,
+                      interleaved: bool = False, stream=None):
+    """Write a step's new keys and values into the pages of their sequences,
+    the keys (and ``q``, if given) rotated by their positions.
+
+    ``k``, ``v`` [total, h_kv, 128] and ``q`` [total, h_q, 128] BF16, each of
+    any token stride (slices of a fused projection).  ``page_table`` int32
+    [batch, max_pages]; ``seqlens_k`` int32 [batch], the sequences' lengths
+    with the new tokens; ``cu_seqlens`` int32 [batch + 1] (None: total /
+    batch rows each); ``max_seqlen`` bounds a sequence's new rows (None:
+    total).  ``inv_freq`` FP32 [rotary_dim / 2] holds the rotation's
+    frequencies (None: none); pairs are (i, i + rotary_dim / 2), or (2i,
+    2i + 1) with ``interleaved``.  Returns the rotated queries [total, h_q,
+    128] (``q_out`` if given), or None without ``q``.
+
+    One launch; rows behind the last sequence are neither read nor written.
+    """
+    import torch
+    total, h_kv = k.shape[0], cache.h_kv
+    k_stride = _packed_rows("k", k, h_kv)
+    v_stride = _packed_rows("v", v, h_kv)
+    if v.shape[0] != total:
+        raise ValueError("k, v shapes disagree")
+    batch, max_pages = _cache_batch(cache, page_table, seqlens_k, cu_seqlens, "cu_seqlens")
+    tensors = dict(k=k, v=v, page_table=page_table, seqlens_k=seqlens_k)
+    h_q, q_stride, rotary_dim = h_kv, 0, 0
+    if q is not None:
+        q_stride, h_q = _packed_rows("q", q), q.shape[1]
+        if q.shape[0] != total:
+            raise ValueError("q, k shapes disagree")
+        tensors["q"] = q
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    if cu_seqlens is not None:
+        tensors["cu_seqlens"] = cu_seqlens
+    if inv_freq is not None:
+        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be a contiguous float32 vector")
+        tensors["inv_freq"], rotary_dim = inv_freq, 2 * inv_freq.numel()
+    dev = _cuda_device(stream, **tensors)
+    if dev != cache.device:
+        raise ValueError(f"the cache is on {cache.device}, the call's tensors on {dev}")
+    if total == 0:
+        return None if q is None else _out(q, q_out, "q_out", q.shape, torch.bfloat16, stream)
+    with _on_device(dev):
+        if q is not None:
+            q_out = _out(q, q_out, "q_out", (total, h_q, 128), torch.bfloat16, stream)
+        rc = load_library().attn_cache_append(
+            cache._ref, k.data_ptr(), v.data_ptr(), None if q is None else q.data_ptr(),
+            None if q is None else q_out.data_ptr(), page_table.data_ptr(), seqlens_k.data_ptr(),
+            None if cu_seqlens is None else cu_seqlens.data_ptr(),
+            None if inv_freq is None else inv_freq.data_ptr(), batch, max_pages, total,
+            int(total if max_seqlen is None else max_seqlen), h_q, k_stride, v_stride, q_stride,
+            rotary_dim, int(bool(interleaved)), _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_cache_append")
+    return q_out
+
+
+def cache_workspace_bytes(h_q, h_kv, max_seqlen_q) -> int:
+    """Workspace bytes of :func:`attn_fwd_cache` on the current device."""
+    return int(load_library().attn_fwd_cache_workspace_bytes(h_q, h_kv, max_seqlen_q))
+
+
+def attn_fwd_cache(q, cache: KVCache, page_table, seqlens_k, cu_seqlens_q=None,
+                   max_seqlen_q: int | None = None, causal: bool = True, window_left: int = -1,
+                   scale: float | None = None, o=None, lse=None, workspace=None, stream=None):
+    """Attention of the packed queries ``q`` [total_q, h_q, 128] BF16 over the
+    pages of their sequences; the other arguments as
+    :func:`attn_cache_append`.  With ``causal`` (the default) the i-th of a
+    sequence's n queries sees keys up to seqlens_k - n + i, with
+    ``window_left`` >= 0 only the last window_left + 1 of them.  Returns (o
+    [total_q, h_q, 128] BF16, lse [h_q, total_q] FP32); a row that sees no key
+    gets 0 and -inf, rows behind the last sequence are left as they were.
+
+    ``workspace``: a CUDA uint8 tensor of at least
+    :func:`cache_workspace_bytes` bytes, allocated here if None.  Two launches.
+    """
+    import torch
+    q_stride = _packed_rows("q", q)
+    total_q, h_q, d = q.shape
+    batch, max_pages = _cache_batch(cache, page_table, seqlens_k, cu_seqlens_q, "cu_seqlens_q")
+    tensors = dict(q=q, page_table=page_table, seqlens_k=seqlens_k)
+    if cu_seqlens_q is not None:
+        tensors["cu_seqlens_q"] = cu_seqlens_q
+    dev = _cuda_device(stream, **tensors)
+    if dev != cache.device:
+        raise ValueError(f"the cache is on {cache.device}, the call's tensors on {dev}")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if max_seqlen_q is None:
+        max_seqlen_q = total_q if cu_seqlens_q is not None else -(-total_q // batch)
+    with _on_device(dev):
+        o, lse = _outputs(q, o, lse, (total_q, h_q, d), (h_q, total_q), stream)
+        if total_q == 0:
+            return o, lse
+        if workspace is None:
+            workspace = _workspace(q, None, cache_workspace_bytes(h_q, cache.h_kv, max_seqlen_q),
+                                   stream)
+        else:
+            workspace = _workspace(q, workspace, 0, stream)
+        rc = load_library().attn_fwd_cache(
+            cache._ref, q.data_ptr(), o.data_ptr(), lse.data_ptr(), page_table.data_ptr(),
+            seqlens_k.data_ptr(), None if cu_seqlens_q is None else cu_seqlens_q.data_ptr(),
+            batch, max_pages, total_q, int(max_seqlen_q), h_q, q_stride, int(bool(causal)),
+            int(window_left), float(scale), workspace.data_ptr(), _nbytes(workspace),
+            _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_fwd_cache")
     return o, lse
 
 

@@ -14,7 +14,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libattn_sm100.so")
-SOURCES = [os.path.join(CSRC, "attn_api.cu")]
+SOURCES = [os.path.join(CSRC, "attn_lib.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [
     os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
 

@@ -1,0 +1,344 @@
+// attn_cache_api.cuh -- the C ABI declared in include/attn_cache.h: argument
+// validation (no CUDA call on an invalid argument), tensor maps of the pools
+// and the launches.  Included after attn_api.cu, whose per-device state and
+// status word it shares.
+#pragma once
+
+#include "attn_cache.h"
+#include "attn_cache_append.cuh"
+#include "attn_cache_kernel.cuh"
+
+namespace {
+
+constexpr long long kMaxInt = 0x7fffffffLL;
+
+// The device's kernels may use their shared memory (set once per device).
+int init_cache_device(int dev, DeviceState** st) {
+    const int rc = init_device(dev, st);
+    if (rc != ATTN_OK) return rc;
+    static bool ready[kMaxDevices] = {};
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (ready[dev]) return ATTN_OK;
+    const auto smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+#define SDPA10_CACHE_SMEM(kE, kR)                                                  \
+    if (cudaFuncSetAttribute(cache::attn_fwd_cache_kernel<kE, kR>, smem,           \
+                             cache::Shape<kE, kR>::kAlloc) != cudaSuccess)         \
+    return ATTN_ERR_CUDA
+    SDPA10_CACHE_SMEM(false, 8);
+    SDPA10_CACHE_SMEM(false, 16);
+    SDPA10_CACHE_SMEM(false, 32);
+    SDPA10_CACHE_SMEM(false, 64);
+    SDPA10_CACHE_SMEM(true, 8);
+    SDPA10_CACHE_SMEM(true, 16);
+    SDPA10_CACHE_SMEM(true, 32);
+    SDPA10_CACHE_SMEM(true, 64);
+#undef SDPA10_CACHE_SMEM
+    ready[dev] = true;
+    return ATTN_OK;
+}
+
+int validate_cache(const attn_cache_t* c) {
+    if (!c || !c->k_pages || !c->v_pages) return ATTN_ERR_INVALID;
+    if (c->type != ATTN_CACHE_BF16 && c->type != ATTN_CACHE_E4M3) return ATTN_ERR_INVALID;
+    const bool e4m3 = c->type == ATTN_CACHE_E4M3;
+    if (e4m3 != (c->k_scale != nullptr) || e4m3 != (c->v_scale != nullptr))
+        return ATTN_ERR_INVALID;
+    if (c->num_pages <= 0 || c->page_size <= 0 || c->h_kv <= 0 || c->d <= 0)
+        return ATTN_ERR_INVALID;
+    if (c->page_size % 8 != 0 || c->page_size > (1 << 20)) return ATTN_ERR_INVALID;
+    if (c->d != kHeadDim) return ATTN_ERR_UNSUPPORTED;
+    const int64_t size = e4m3 ? 1 : 2;
+    for (const int64_t s : {c->page_stride, c->token_stride, c->head_stride})
+        if (s <= 0 || s % (16 / size) != 0 || s >= (int64_t{1} << 40) / size)
+            return ATTN_ERR_INVALID;
+    if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16) ||
+        (e4m3 && (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))))
+        return ATTN_ERR_ALIGN;
+    return ATTN_OK;
+}
+
+// What the two entry points share: the packed batch and its table.
+int validate_batch(const attn_cache_t* c, const int* page_table, const int* seqlens_k,
+                   const int* cu, int batch, int max_pages, int total, int max_seqlen, int h_q) {
+    if (!page_table || !seqlens_k) return ATTN_ERR_INVALID;
+    if (batch <= 0 || max_pages <= 0 || total <= 0 || max_seqlen <= 0 || h_q <= 0)
+        return ATTN_ERR_INVALID;
+    if (h_q % c->h_kv != 0) return ATTN_ERR_INVALID;
+    if (!cu && total % batch != 0) return ATTN_ERR_INVALID;
+    if (!aligned(page_table, 4) || !aligned(seqlens_k, 4) || (cu && !aligned(cu, 4)))
+        return ATTN_ERR_ALIGN;
+    return ATTN_OK;
+}
+
+bool token_stride_ok(int64_t stride, int heads, int total) {
+    return stride % 8 == 0 && stride >= (total > 1 ? static_cast<int64_t>(heads) * kHeadDim : 0) &&
+           stride < (int64_t{1} << 39);
+}
+
+// [num_pages, page_size, h_kv, 128] of the pool as a 4-D map {d, heads,
+// tokens, pages}; a box is `box` tokens of one head, 128 bytes of each.
+bool encode_pool(CUtensorMap* m, const attn_cache_t* c, void* base, int box) {
+    const bool e4m3 = c->type == ATTN_CACHE_E4M3;
+    const cuuint64_t size = e4m3 ? 1 : 2;
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(c->h_kv),
+                          static_cast<cuuint64_t>(c->page_size),
+                          static_cast<cuuint64_t>(c->num_pages)};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(c->head_stride) * size,
+                             static_cast<cuuint64_t>(c->token_stride) * size,
+                             static_cast<cuuint64_t>(c->page_stride) * size};
+    cuuint32_t bx[4] = {e4m3 ? 128u : 64u, 1, static_cast<cuuint32_t>(box), 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return g_encode(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                    base, dims, strides, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Query rows of a tile: the smallest of 8, 16, 32 and 64 that holds a
+// sequence's rows of one key/value head.
+int cache_rows(int group, int max_seqlen) {
+    const long long rows = static_cast<long long>(group) * max_seqlen;
+    return rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : 64));
+}
+
+constexpr int kCacheCtasPerSm = 2;  // of any variant, at most
+
+struct CacheWorkspace {
+    size_t ml, o, bytes;  // offsets; the shares' records come first
+};
+CacheWorkspace cache_workspace(int sms, int rows) {
+    const size_t ctas = static_cast<size_t>(sms) * kCacheCtasPerSm;
+    CacheWorkspace w;
+    w.ml = round_up(ctas * sizeof(int4), 256);
+    w.o = w.ml + round_up(ctas * 2 * rows * sizeof(float2), 256);
+    w.bytes = w.o + ctas * 2 * rows * kHeadDim * sizeof(float);
+    return w;
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
+                         cudaStream_t stream, Args... args) {
+    // The launch may begin while the kernel before it ends: the kernels wait
+    // for it themselves (griddepcontrol) before they touch any data.
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <bool kE, int kR>
+int launch_fwd_cache(const CUtensorMap& tk, const CUtensorMap& tv, const cache::FwdCacheParams& p,
+                     int sms, long long most_units, cudaStream_t cs) {
+    using S = cache::Shape<kE, kR>;
+    static_assert(S::kCtasPerSm <= kCacheCtasPerSm, "the workspace holds a part of each CTA");
+    const long long all = static_cast<long long>(sms) * S::kCtasPerSm;
+    const unsigned grid = static_cast<unsigned>(most_units < all ? most_units : all);
+    if (launch_after(cache::attn_fwd_cache_kernel<kE, kR>, dim3(grid), S::kThreads, S::kAlloc, cs,
+                     tk, tv, p) != cudaSuccess)
+        return ATTN_ERR_CUDA;
+    if (launch_after(cache::attn_cache_merge_kernel<kR>, dim3(grid, 8), cache::kMergeWarps * 32, 0,
+                     cs, p) != cudaSuccess)
+        return ATTN_ERR_CUDA;
+    g_last_launches = 2;
+    return ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" int attn_cache_append(const attn_cache_t* c, const void* k, const void* v,
+                                 const void* q, void* q_out, const int* page_table,
+                                 const int* seqlens_k, const int* cu_seqlens,
+                                 const float* inv_freq, int batch, int max_pages, int total,
+                                 int max_seqlen, int h_q, int64_t k_stride, int64_t v_stride,
+                                 int64_t q_stride, int rotary_dim, int interleaved,
+                                 void* stream) {
+    int rc = validate_cache(c);
+    if (rc != ATTN_OK) return rc;
+    if (!k || !v || !q != !q_out) return ATTN_ERR_INVALID;
+    rc = validate_batch(c, page_table, seqlens_k, cu_seqlens, batch, max_pages, total, max_seqlen,
+                        h_q);
+    if (rc != ATTN_OK) return rc;
+    if (rotary_dim < 0 || rotary_dim > kHeadDim || rotary_dim % 16 != 0 ||
+        (rotary_dim > 0) != (inv_freq != nullptr) || (interleaved != 0 && interleaved != 1))
+        return ATTN_ERR_INVALID;
+    if (!token_stride_ok(k_stride, c->h_kv, total) || !token_stride_ok(v_stride, c->h_kv, total) ||
+        (q && !token_stride_ok(q_stride, h_q, total)))
+        return ATTN_ERR_INVALID;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16) ||
+        !aligned(inv_freq, 4))
+        return ATTN_ERR_ALIGN;
+
+    const bool e4m3 = c->type == ATTN_CACHE_E4M3;
+    cache::AppendParams p{};
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k = static_cast<const __nv_bfloat16*>(k);
+    p.v = static_cast<const __nv_bfloat16*>(v);
+    p.q_out = static_cast<__nv_bfloat16*>(q_out);
+    p.k_pages = static_cast<uint8_t*>(c->k_pages);
+    p.v_pages = static_cast<uint8_t*>(c->v_pages);
+    p.k_scale = c->k_scale;
+    p.v_scale = c->v_scale;
+    p.table = page_table;
+    p.seqlens = seqlens_k;
+    p.cu = cu_seqlens;
+    p.inv_freq = inv_freq;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.page_stride = c->page_stride;
+    p.token_stride = c->token_stride;
+    p.head_stride = c->head_stride;
+    p.batch = batch;
+    p.max_pages = max_pages;
+    p.total = total;
+    p.n_uniform = total / batch;
+    const int most = std::min(max_seqlen, cu_seqlens ? total : p.n_uniform);
+    p.max_seqlen = most;
+    p.h_q = q ? h_q : 0;
+    p.h_kv = c->h_kv;
+    p.num_pages = c->num_pages;
+    p.page_size = c->page_size;
+    p.rotary_dim = rotary_dim;
+    p.interleaved = interleaved;
+    p.row_heads = p.h_q + (e4m3 ? 0 : 2 * c->h_kv);
+
+    // Page role: n rows enter at most (n + page_size - 2) / page_size + 1 pages.
+    p.pages_per_seq = static_cast<int>((static_cast<long long>(most) + c->page_size - 2) / c->page_size) + 1;
+    const long long page_blocks =
+        e4m3 ? static_cast<long long>(batch) * p.pages_per_seq * c->h_kv : 0;
+    const int threads = e4m3 && most <= 8 ? 64 : (e4m3 && most <= 16 ? 128 : 256);
+    // Row role: one head for 8 lanes while that leaves SMs idle, more heads
+    // (whose angles are computed once) when there are rows enough.
+    p.heads_per_unit = 1;
+    while (p.heads_per_unit < 8 &&
+           static_cast<long long>(total) * p.row_heads / (2 * p.heads_per_unit) >= 148LL * 2048 / 8)
+        p.heads_per_unit *= 2;
+    const long long units =
+        p.row_heads == 0 ? 0
+                         : static_cast<long long>(total) *
+                               ((p.row_heads + p.heads_per_unit - 1) / p.heads_per_unit);
+    const long long row_blocks = (units * 8 + threads - 1) / threads;
+    if (page_blocks + row_blocks > kMaxInt) return ATTN_ERR_INVALID;
+    p.page_blocks = static_cast<int>(page_blocks);
+    if (page_blocks + row_blocks == 0) return ATTN_OK;
+
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
+    DeviceState* st = nullptr;
+    rc = init_device(dev, &st);
+    if (rc != ATTN_OK) return rc;
+    cache::attn_cache_append_kernel<<<static_cast<unsigned>(page_blocks + row_blocks),
+                                      static_cast<unsigned>(threads), 0,
+                                      static_cast<cudaStream_t>(stream)>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+    g_last_launches = 1;
+    return ATTN_OK;
+}
+
+extern "C" size_t attn_fwd_cache_workspace_bytes(int h_q, int h_kv, int max_seqlen_q) {
+    if (h_q <= 0 || h_kv <= 0 || h_q % h_kv != 0 || max_seqlen_q <= 0) return 0;
+    int dev = 0;
+    DeviceState* st = nullptr;
+    if (cudaGetDevice(&dev) != cudaSuccess || init_device(dev, &st) != ATTN_OK) return 0;
+    return cache_workspace(st->num_sms, cache_rows(h_q / h_kv, max_seqlen_q)).bytes;
+}
+
+extern "C" int attn_fwd_cache(const attn_cache_t* c, const void* q, void* o, float* lse,
+                              const int* page_table, const int* seqlens_k,
+                              const int* cu_seqlens_q, int batch, int max_pages, int total_q,
+                              int max_seqlen_q, int h_q, int64_t q_stride, int causal,
+                              int window_left, float scale, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+    int rc = validate_cache(c);
+    if (rc != ATTN_OK) return rc;
+    if (!q || !o || !lse || !workspace) return ATTN_ERR_INVALID;
+    rc = validate_batch(c, page_table, seqlens_k, cu_seqlens_q, batch, max_pages, total_q,
+                        max_seqlen_q, h_q);
+    if (rc != ATTN_OK) return rc;
+    if (!std::isfinite(scale) || (causal != 0 && causal != 1)) return ATTN_ERR_INVALID;
+    if (window_left < -1 || (window_left >= 0 && !causal)) return ATTN_ERR_INVALID;
+    if (!token_stride_ok(q_stride, h_q, total_q)) return ATTN_ERR_INVALID;
+    if (static_cast<long long>(total_q) * h_q > kMaxInt) return ATTN_ERR_INVALID;
+    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 256))
+        return ATTN_ERR_ALIGN;
+
+    cache::FwdCacheParams p{};
+    p.batch = batch;
+    p.max_pages = max_pages;
+    p.total_q = total_q;
+    p.n_uniform = total_q / batch;
+    p.max_seqlen_q = std::min(max_seqlen_q, cu_seqlens_q ? total_q : p.n_uniform);
+    p.h_q = h_q;
+    p.h_kv = c->h_kv;
+    p.group = h_q / c->h_kv;
+    const int rows = cache_rows(p.group, p.max_seqlen_q);
+    p.heads_per_tile = std::min(p.group, rows);
+    p.q_per_tile = rows / p.heads_per_tile;
+    p.head_tiles = (p.group + p.heads_per_tile - 1) / p.heads_per_tile;
+    // The share of a CTA has 32-bit numbers of units (row tiles x key tiles).
+    const long long cap = static_cast<long long>(max_pages) * c->page_size;
+    const long long key_tiles = std::min(cap, kMaxInt) / 128 + 1;
+    const long long row_tiles =
+        (cu_seqlens_q ? std::min(static_cast<long long>(total_q) / p.q_per_tile + batch,
+                                 static_cast<long long>(batch) *
+                                     ((p.max_seqlen_q + p.q_per_tile - 1) / p.q_per_tile))
+                      : static_cast<long long>(batch) *
+                            ((p.max_seqlen_q + p.q_per_tile - 1) / p.q_per_tile)) *
+        c->h_kv * p.head_tiles;
+    if (row_tiles > kMaxInt || row_tiles * key_tiles / 64 > kMaxInt) return ATTN_ERR_INVALID;
+
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
+    DeviceState* st = nullptr;
+    rc = init_cache_device(dev, &st);
+    if (rc != ATTN_OK) return rc;
+    const CacheWorkspace w = cache_workspace(st->num_sms, rows);
+    if (workspace_bytes < w.bytes) return ATTN_ERR_INVALID;
+
+    const int low = c->page_size & -c->page_size;
+    p.box = std::min(low, 128);
+    p.num_pages = c->num_pages;
+    p.page_size = c->page_size;
+    p.div_page = FastDiv::make(static_cast<uint32_t>(c->page_size));
+    CUtensorMap tk, tv;
+    if (!encode_pool(&tk, c, c->k_pages, p.box) || !encode_pool(&tv, c, c->v_pages, p.box))
+        return ATTN_ERR_CUDA;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.k_scale = c->k_scale;
+    p.v_scale = c->v_scale;
+    p.table = page_table;
+    p.seqlens = seqlens_k;
+    p.cu = cu_seqlens_q;
+    p.q_stride = q_stride;
+    p.causal = causal;
+    p.window = window_left;
+    p.scale_log2 = scale * 1.44269504088896341f;
+    char* ws = static_cast<char*>(workspace);
+    p.meta = reinterpret_cast<int4*>(ws);
+    p.part_ml = reinterpret_cast<float2*>(ws + w.ml);
+    p.part_o = reinterpret_cast<float*>(ws + w.o);
+    p.timeout_ns = g_timeout_ns;
+    p.status = st->status;
+    const long long most = row_tiles * key_tiles;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const int sms = st->num_sms;
+    if (c->type == ATTN_CACHE_E4M3) {
+        if (rows == 8) return launch_fwd_cache<true, 8>(tk, tv, p, sms, most, cs);
+        if (rows == 16) return launch_fwd_cache<true, 16>(tk, tv, p, sms, most, cs);
+        if (rows == 32) return launch_fwd_cache<true, 32>(tk, tv, p, sms, most, cs);
+        return launch_fwd_cache<true, 64>(tk, tv, p, sms, most, cs);
+    }
+    if (rows == 8) return launch_fwd_cache<false, 8>(tk, tv, p, sms, most, cs);
+    if (rows == 16) return launch_fwd_cache<false, 16>(tk, tv, p, sms, most, cs);
+    if (rows == 32) return launch_fwd_cache<false, 32>(tk, tv, p, sms, most, cs);
+    return launch_fwd_cache<false, 64>(tk, tv, p, sms, most, cs);
+}

@@ -1,0 +1,1055 @@
+// attn_cache_kernel.cuh -- attention of a packed batch of queries over a paged
+// key/value cache (BF16, or E4M3 with a scale for each page and head).
+//
+// For few query rows over many keys the work is reading the cache once, so the
+// products are laid out with the keys and the head dim on the 128 rows of the
+// tensor core's tile and the query rows on its narrow side:
+//     S^T [128 keys x R rows] = K Q^T        (A = K tile,   B = Q)
+//     O^T [128 dims x R rows] += V^T P^T     (A = V tile^T, B = P)
+// K and V tiles go from the pages to shared memory by TMA and to the tensor
+// core as they are, in either type.  A thread owns one key of the tile: the
+// scale of its page is one factor for it, and the weights of its R rows are R
+// contiguous bytes (or BF16 values) of its row of P.
+//
+// E4M3 pages (kind::f8f6f4): Q, scaled by a power of two to a largest element
+// in [128, 256), is a sum of two E4M3 numbers; a weight, rounded to FP16, is a
+// sum of three E5M2 numbers (an E5M2 number is the high byte of an FP16
+// number: each takes the next three significant bits).  The pieces are further
+// K steps into the same accumulators.
+//
+// Softmax: the weights of row c are 2^(y - M_c) with y = scale log2(e) q.k ks
+// + log2(vs), so V's scale rides in the exponent and the row sum takes it out
+// again.  M_c is an integer that all threads share, raised only when a weight
+// would pass 2^kSlack.
+//
+// Work: a CTA takes a contiguous share of all (sequence, head, row tile, key
+// tile) units; items cut by a share's border leave FP32 partials that
+// attn_cache_merge_kernel joins in order.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math_constants.h>
+
+#include <cstdint>
+
+#include "attn_cache_append.cuh"
+#include "attn_common.cuh"
+
+namespace sdpa10 {
+namespace cache {
+
+constexpr int kMaxRows = 64;       // query rows of the widest tile
+constexpr int kMinChunk = 1;       // least key tiles of a CTA's share
+constexpr float kSlack = 4.f;      // log2 of the largest weight over 2^M
+constexpr float kBiasE4M3 = 11.f;  // weights are kept as 2^11 p: below 2^15 in FP16 and E5M2
+
+struct FwdCacheParams {
+    const __nv_bfloat16* q;
+    __nv_bfloat16* o;
+    float* lse;
+    const float* k_scale;
+    const float* v_scale;
+    const int* table;
+    const int* seqlens;
+    const int* cu;  // null: n_uniform rows each
+    long long q_stride;
+    int batch, max_pages, total_q, max_seqlen_q, n_uniform;
+    int h_q, h_kv, group, num_pages, page_size;
+    FastDiv div_page;
+    int box;             // keys of one TMA copy: the power of two that divides page_size, <= 128
+    int heads_per_tile;  // query heads of a row tile
+    int q_per_tile;      // queries of a row tile
+    int head_tiles;      // row tiles across the group's heads
+    int causal, window;  // window -1: none
+    float scale_log2;    // scale * log2(e)
+    float* part_o;       // [ctas][2][R][128]
+    float2* part_ml;     // [ctas][2][R]: log2 of the unit of weights, row sum in it
+    int4* meta;          // [ctas]: the item that begins in the share and goes on after it
+    unsigned long long timeout_ns;
+    unsigned int* status;
+};
+
+// ------------------------------------------------------------------ schedule
+struct Seq {
+    int row0, n;    // its rows of the packed batch
+    int len, kv;    // its length, and the keys the table has room for
+    int tiles;      // row tiles along its queries
+};
+
+__device__ __forceinline__ Seq load_seq(const FwdCacheParams& p, int b) {
+    Seq s;
+    if (p.cu != nullptr) {
+        const int r0 = p.cu[b], r1 = p.cu[b + 1];
+        s.row0 = min(max(r0, 0), p.total_q);
+        s.n = min(max(r1, s.row0), p.total_q) - s.row0;
+    } else {
+        s.row0 = b * p.n_uniform;
+        s.n = p.n_uniform;
+    }
+    s.len = max(p.seqlens[b], 0);
+    const long long cap = static_cast<long long>(p.max_pages) * p.page_size;
+    s.kv = s.len < cap ? s.len : static_cast<int>(cap);
+    s.tiles = (min(s.n, p.max_seqlen_q) + p.q_per_tile - 1) / p.q_per_tile;
+    return s;
+}
+
+// Queries [i0, i1] of a sequence and the keys [beg, end) that any of them sees.
+struct RowTile {
+    int i0, i1, beg, end, tile0, n;  // first 128-key tile and how many (at least one)
+};
+
+__device__ __forceinline__ RowTile row_tile(const FwdCacheParams& p, const Seq& s, int t) {
+    RowTile r;
+    r.i0 = t * p.q_per_tile;
+    r.i1 = min(r.i0 + p.q_per_tile, min(s.n, p.max_seqlen_q)) - 1;
+    const int shift = s.len - s.n;
+    r.end = p.causal ? min(s.kv, max(shift + r.i1 + 1, 0)) : s.kv;
+    r.beg = p.window >= 0 ? max(0, shift + r.i0 - p.window) : 0;
+    r.tile0 = r.beg >> 7;
+    r.n = r.end > r.beg ? ((r.end + 127) >> 7) - r.tile0 : 1;
+    return r;
+}
+
+__device__ __forceinline__ long long seq_units(const FwdCacheParams& p, const Seq& s) {
+    long long u = 0;
+    for (int t = 0; t < s.tiles; ++t) u += row_tile(p, s, t).n;
+    return u;
+}
+
+// A CTA's place in the work: item (b, h, t), key tiles [j, j + m) of it.
+struct Cursor {
+    int b, h, t, j;
+    int left;  // units of the share from here on
+};
+
+struct Item {
+    Seq s;
+    RowTile r;
+    int m;
+};
+
+__device__ __forceinline__ Item cursor_item(const FwdCacheParams& p, const Cursor& c) {
+    Item it;
+    it.s = load_seq(p, c.b);
+    it.r = row_tile(p, it.s, c.t);
+    it.m = min(it.r.n - c.j, c.left);
+    return it;
+}
+
+__device__ __forceinline__ void cursor_next(const FwdCacheParams& p, Cursor& c, const Item& it) {
+    c.left -= it.m;
+    c.j = 0;
+    if (++c.t < it.s.tiles) return;
+    c.t = 0;
+    if (++c.h < p.h_kv * p.head_tiles) return;
+    c.h = 0;
+    while (c.left > 0 && ++c.b < p.batch && load_seq(p, c.b).tiles == 0) {
+    }
+    if (c.b >= p.batch) c.left = 0;
+}
+
+// ------------------------------------------------------------------ PTX
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* m, uint32_t bar,
+                                              int c0, int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+// kind::f8f6f4 issued by one elected lane of a converged warp.
+__device__ __forceinline__ void mma_f8_warp(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+
+// 32 lanes x 8 or 16 consecutive columns.
+__device__ __forceinline__ void tmem_load(uint32_t t, float (&r)[8]) {
+    uint32_t u[8];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+          "=r"(u[7])
+        : "r"(t));
+    ptx::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = __uint_as_float(u[i]);
+}
+__device__ __forceinline__ void tmem_load(uint32_t t, float (&r)[16]) {
+    uint32_t u[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15}, [%16];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+          "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]),
+          "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(t));
+    ptx::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __uint_as_float(u[i]);
+}
+__device__ __forceinline__ void tmem_store(uint32_t t, const float (&r)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t),
+        "r"(__float_as_uint(r[0])), "r"(__float_as_uint(r[1])), "r"(__float_as_uint(r[2])),
+        "r"(__float_as_uint(r[3])), "r"(__float_as_uint(r[4])), "r"(__float_as_uint(r[5])),
+        "r"(__float_as_uint(r[6])), "r"(__float_as_uint(r[7]))
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store(uint32_t t, const float (&r)[16]) {
+    float a[8], b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        a[i] = r[i];
+        b[i] = r[8 + i];
+    }
+    tmem_store(t, a);
+    tmem_store(t + 8, b);
+}
+
+// Barrier of 128 threads that also tells whether any of them says yes.
+__device__ __forceinline__ bool group_any(int id, bool yes) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.aligned.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(yes ? 1u : 0u), "r"(id)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void group_sync(int id) {
+    asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(id) : "memory");
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t d;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// ------------------------------------------------------------------ layout
+// kE: E4M3 pages.  kR: query rows of a tile.
+template <bool kE, int kR>
+struct Shape {
+    static constexpr int kN = kR < 16 ? 16 : kR;          // the MMA's narrow side
+    static constexpr int kGroups = kR > 32 ? 2 : 1;       // column groups of four softmax warps
+    static constexpr int kCols = kR / kGroups;            // columns of a thread
+    static constexpr int kSub = kCols < 16 ? kCols : 16;  // columns worked on at a time
+    static constexpr int kSoftThreads = 128 * kGroups;
+    static constexpr int kThreads = kSoftThreads + 64;
+    static constexpr int kQPieces = kE ? 2 : 1, kPPieces = kE ? 3 : 1;
+    static constexpr int kElem = kE ? 1 : 2;
+    static constexpr int kTile = 128 * kHeadDim * kElem;  // a K or V tile
+    static constexpr int kQPiece = kN * kHeadDim * kElem;
+    // P: rows of 128 bytes, one per key.  Piece i of E4M3 starts kN bytes after
+    // the one before; three of 64 columns need a second buffer.
+    static constexpr int kPBuf = 128 * 128;
+    static constexpr int kPBytes = (kPPieces * kN * kElem > 128 ? 2 : 1) * kPBuf;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffP = kOffQ + (kQPieces * kQPiece + 1023) / 1024 * 1024;
+    static constexpr int kOffRing = kOffP + kPBytes;
+    static constexpr int kTail = 3072;  // barriers and the small arrays below
+    // Two CTAs of an SM overlap one's softmax with the other's products.  Ring
+    // and P of BF16 pages leave room for one, whose deeper ring has the same
+    // bytes in flight.
+    static constexpr int kCtasPerSm = kE ? 2 : 1;
+    static constexpr int kBudget = (kE ? 113 : 227) * 1024 - 1024;
+    static constexpr int kSlots = (kBudget - kOffRing - kTail) / kTile;
+    static_assert(kSlots >= 3 && kSlots <= 8, "the ring needs K(j+1) beside K(j) and V(j)");
+    static constexpr int kOffTail = kOffRing + kSlots * kTile;
+    static constexpr int kAlloc = kOffTail + kTail + 1024;
+    static constexpr uint32_t kTmemCols = 3 * kN <= 64 ? 64 : (3 * kN <= 128 ? 128 : 256);
+    __host__ __device__ static constexpr int p_offset(int piece) {
+        const int at = piece * kN * kElem;
+        return at + kN * kElem <= 128 ? at : kPBuf + at - 128;
+    }
+};
+
+struct Tail {
+    uint64_t full[8], empty[8];
+    uint64_t q_full, s_full[2], s_free[2], p_full, pv_done, drain;
+    uint32_t tmem;
+    int abort;
+    Cursor cursor;
+    int chunk;              // units of every share
+    long long begin;        // first unit of this one
+    long long wsum[16];
+    float qf[kMaxRows];     // E4M3: 2^-e of the row's scaling of Q
+    float neg_m[kMaxRows];  // minus log2 of the row's unit of weights
+    float limit[kMaxRows];  // largest y that leaves the unit as it is; -inf: no key seen yet
+    float wmax[4][kMaxRows];
+    int last[kMaxRows];     // last key the row sees
+    int first[kMaxRows];    // first one
+    int row[kMaxRows];      // query * h_q + head; -1: no such row
+};
+static_assert(sizeof(Tail) <= 3072, "");
+
+// Where this CTA's share of the units begins (every thread of the CTA calls).
+template <int kThreads>
+__device__ __forceinline__ void find_share(const FwdCacheParams& p, Tail& tl) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per_seq = p.h_kv * p.head_tiles;
+    constexpr int kWarps = kThreads / 32;
+    long long mine = 0;
+    for (int b = tid; b < p.batch; b += kThreads) mine += seq_units(p, load_seq(p, b));
+    long long v = mine;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0) tl.wsum[warp] = v;
+    __syncthreads();
+    long long total = 0;
+    for (int w = 0; w < kWarps; ++w) total += tl.wsum[w];
+    total *= per_seq;
+    long long chunk = (total + gridDim.x - 1) / gridDim.x;
+    if (chunk < kMinChunk) chunk = kMinChunk;
+    const long long begin = chunk * blockIdx.x;
+    if (tid == 0) {
+        const long long rest = total - begin;
+        tl.cursor.left = static_cast<int>(rest < 0 ? 0 : (rest < chunk ? rest : chunk));
+        tl.chunk = static_cast<int>(chunk);
+        tl.begin = begin;
+    }
+    if (begin >= total) {
+        __syncthreads();
+        return;
+    }
+    long long run = 0;
+    for (int base = 0; base < p.batch; base += kThreads) {
+        const int b = base + tid;
+        long long own = 0;
+        if (p.batch <= kThreads) own = mine;
+        else if (b < p.batch) own = seq_units(p, load_seq(p, b));
+        long long inc = own * per_seq;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += up;
+        }
+        __syncthreads();  // the sums of the pass before have been read
+        if (lane == 31) tl.wsum[warp] = inc;
+        __syncthreads();
+        long long all = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) inc += tl.wsum[w];
+            all += tl.wsum[w];
+        }
+        inc += run;
+        const long long exc = inc - own * per_seq;
+        if (begin >= exc && begin < inc) {
+            const long long rem = begin - exc;
+            const Seq s = load_seq(p, b);
+            int left = static_cast<int>(rem % own), t = 0;
+            for (;; ++t) {
+                const int n = row_tile(p, s, t).n;
+                if (left < n) break;
+                left -= n;
+            }
+            tl.cursor.b = b;
+            tl.cursor.h = static_cast<int>(rem / own);
+            tl.cursor.t = t;
+            tl.cursor.j = left;
+        }
+        run += all;
+        if (run > begin) break;  // the same for every thread
+    }
+    __syncthreads();
+}
+
+// ------------------------------------------------------------------ producer
+// One warp: lane i loads the tile's i-th box of page_size-dividing keys.
+template <bool kE, int kR>
+__device__ __forceinline__ void producer_role(const FwdCacheParams& p, const CUtensorMap* tm_k,
+                                              const CUtensorMap* tm_v, Tail& tl, uint32_t ring,
+                                              const WaitCtx& wc, int lane) {
+    using S = Shape<kE, kR>;
+    const int boxes = 128 / p.box;
+    const uint32_t box_bytes = static_cast<uint32_t>(p.box) * 128u;  // of one 128-byte column
+    uint32_t loads = 0;
+    bool ok = true;
+    Cursor c = tl.cursor;
+    while (ok && c.left > 0) {
+        const Item it = cursor_item(p, c);
+        const int head = c.h / p.head_tiles;
+        const int* table = p.table + static_cast<long long>(c.b) * p.max_pages;
+        auto page_of = [&](int tile) -> int {  // this lane's page; -1 past the last key
+            const int key = (it.r.tile0 + c.j + tile) * 128 + lane * p.box;
+            return lane < boxes && key < it.r.end ? table[p.div_page.div(key)] : -1;
+        };
+        auto load = [&](const CUtensorMap* tm, int tile, int page) -> bool {
+            const int slot = loads % S::kSlots;
+            if (!wait_bar_warp(ptx::smem_u32(&tl.empty[slot]), ((loads / S::kSlots) & 1) ^ 1, wc))
+                return false;
+            const int key = (it.r.tile0 + c.j + tile) * 128 + lane * p.box;
+            const bool mine = lane < boxes && key < it.r.end;
+            const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));
+            const uint32_t bar = ptx::smem_u32(&tl.full[slot]);
+            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, n * box_bytes * S::kElem);
+            __syncwarp();
+            if (mine) {
+                const uint32_t dst = ring + slot * S::kTile + lane * box_bytes;
+                const int at = key - p.div_page.div(key) * p.page_size;
+                tma_load_page(dst, tm, bar, 0, head, at, page);
+                if constexpr (!kE) tma_load_page(dst + 16384, tm, bar, 64, head, at, page);
+            }
+            ++loads;
+            return true;
+        };
+        int page = page_of(0);
+        ok = load(tm_k, 0, page);
+        for (int i = 0; i < it.m && ok; ++i) {
+            int next = 0;
+            if (i + 1 < it.m) {
+                next = page_of(i + 1);
+                ok = load(tm_k, i + 1, next);
+            }
+            if (ok) ok = load(tm_v, i, page);
+            page = next;
+        }
+        cursor_next(p, c, it);
+    }
+    // Every copy must land before the CTA may exit.
+    for (uint32_t i = 0; i < S::kSlots && i < loads; ++i) {
+        const uint32_t f = loads - 1 - i;
+        wait_slow(ptx::smem_u32(&tl.full[f % S::kSlots]), (f / S::kSlots) & 1, wc, false);
+    }
+    __syncwarp();
+}
+
+// ------------------------------------------------------------------ MMA
+template <bool kE, int kR>
+__device__ __forceinline__ void mma_role(const FwdCacheParams& p, Tail& tl, uint32_t sq,
+                                         uint32_t sp, uint32_t ring, uint32_t tmem,
+                                         const WaitCtx& wc) {
+    using S = Shape<kE, kR>;
+    // A = K or V^T (128 rows), B = Q or P (kN rows); P's pieces are E5M2 (code 1).
+    constexpr uint32_t kIdQK =
+        kE ? idesc_e4m3_f32(128, S::kN, 0, 0) : idesc_bf16_f32(128, S::kN, 0, 0);
+    constexpr uint32_t kIdPV = kE ? idesc_e4m3_f32(128, S::kN, 1, 1) | (1u << 10)
+                                  : idesc_bf16_f32(128, S::kN, 1, 1);
+    const uint32_t o_tm = tmem + 2 * S::kN;
+    uint32_t used = 0;   // ring tiles taken
+    uint32_t g = 0;      // score tiles issued
+    uint32_t pv = 0;     // weight tiles consumed
+    uint32_t items = 0;
+    bool ok = true;
+    auto wait_tile = [&]() -> bool {
+        return wait_bar_warp(ptx::smem_u32(&tl.full[used % S::kSlots]), (used / S::kSlots) & 1,
+                             wc);
+    };
+    auto qk = [&]() -> bool {
+        if (!wait_tile()) return false;
+        if (g >= 2 && !wait_bar_warp(ptx::smem_u32(&tl.s_free[g & 1]), ((g >> 1) - 1) & 1, wc))
+            return false;
+        ptx::tc_fence_after();
+        const uint32_t s_tm = tmem + (g & 1) * S::kN;
+        const uint32_t ka = desc_lo_sw128(ring + (used % S::kSlots) * S::kTile, 16);
+        if constexpr (kE) {
+#pragma unroll
+            for (int i = 0; i < S::kQPieces; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_f8_warp(s_tm, desc_from_lo(ka + 2 * k),
+                                desc_from_lo(desc_lo_sw128(sq + i * S::kQPiece, 16) + 2 * k),
+                                kIdQK, i + k > 0 ? 1u : 0u);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                ptx::mma_ss_warp(
+                    s_tm, desc_from_lo(ka + (((k >> 2) * 16384 + (k & 3) * 32) >> 4)),
+                    desc_from_lo(desc_lo_sw128(sq, 16) +
+                                 (((k >> 2) * S::kN * 128 + (k & 3) * 32) >> 4)),
+                    kIdQK, k > 0 ? 1u : 0u);
+        }
+        ptx::mma_commit_warp(ptx::smem_u32(&tl.s_full[g & 1]));
+        ptx::mma_commit_warp(ptx::smem_u32(&tl.empty[used % S::kSlots]));
+        ++used;
+        ++g;
+        return true;
+    };
+    auto weigh = [&](bool accumulate) -> bool {
+        if (!wait_tile()) return false;
+        if (!wait_bar_warp(ptx::smem_u32(&tl.p_full), pv & 1, wc)) return false;
+        ptx::tc_fence_after();
+        // Head dim (V) and query rows (P) lie along the 128-byte rows, keys
+        // across them: 8 keys are 1 KiB.
+        const uint32_t va =
+            desc_lo_sw128(ring + (used % S::kSlots) * S::kTile, kE ? S::kTile : 16384);
+        constexpr int kSteps = kE ? 4 : 8, kStepBytes = kE ? 4096 : 2048;
+#pragma unroll
+        for (int i = 0; i < S::kPPieces; ++i)
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                const uint64_t a = desc_from_lo(va + ((k * kStepBytes) >> 4));
+                const uint64_t b = desc_from_lo(desc_lo_sw128(sp + S::p_offset(i), 16384) +
+                                                ((k * kStepBytes) >> 4));
+                const uint32_t acc = accumulate || i + k > 0 ? 1u : 0u;
+                if constexpr (kE) mma_f8_warp(o_tm, a, b, kIdPV, acc);
+                else ptx::mma_ss_warp(o_tm, a, b, kIdPV, acc);
+            }
+        ptx::mma_commit_warp(ptx::smem_u32(&tl.pv_done));
+        ptx::mma_commit_warp(ptx::smem_u32(&tl.empty[used % S::kSlots]));
+        ++used;
+        ++pv;
+        return true;
+    };
+    Cursor c = tl.cursor;
+    while (ok && c.left > 0) {
+        const Item it = cursor_item(p, c);
+        ok = wait_bar_warp(ptx::smem_u32(&tl.q_full), items & 1, wc);
+        ++items;
+        if (ok) ok = qk();
+        for (int i = 0; i < it.m && ok; ++i) {
+            if (i + 1 < it.m) ok = qk();  // the next scores first: softmax waits for them
+            if (ok) ok = weigh(i > 0);
+        }
+        cursor_next(p, c, it);
+    }
+    // All products are done before Tensor Memory is freed.
+    ptx::mma_commit_warp(ptx::smem_u32(&tl.drain));
+    wait_slow(ptx::smem_u32(&tl.drain), 0, wc, false);
+    __syncwarp();
+}
+
+// ------------------------------------------------------------------ softmax
+// Sums over the warp's lanes of kC values each: lane i gets the sum of column
+// i % kC (halves of the columns are exchanged until one is left).
+template <int kC>
+__device__ __forceinline__ float lane_sums(float (&v)[kC], int lane) {
+#pragma unroll
+    for (int half = kC / 2; half > 0; half >>= 1) {
+        const bool up = lane & half;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const float send = up ? v[i] : v[i + half];
+            const float keep = up ? v[i + half] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, half);
+        }
+    }
+    float r = v[0];
+#pragma unroll
+    for (int o = 16; o >= kC; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+    return r;
+}
+
+// The queries of an item's rows [c0, c0 + kCols) into shared memory, and what
+// the rows see.  128 threads.
+template <bool kE, int kR>
+__device__ __forceinline__ void load_rows(const FwdCacheParams& p, Tail& tl, uint8_t* sq,
+                                          const Item& it, int h, int c0, int r) {
+    using S = Shape<kE, kR>;
+    const int head0 = (h % p.head_tiles) * p.heads_per_tile;  // in the group
+    const int heads = min(p.heads_per_tile, p.group - head0);
+    const int kv_head = h / p.head_tiles;
+    const int queries = it.r.i1 - it.r.i0 + 1;
+    const int shift = it.s.len - it.s.n;
+    if (r < S::kCols) {
+        const int c = c0 + r;
+        const int qi = c / p.heads_per_tile, e = c - qi * p.heads_per_tile;
+        const bool there = qi < queries && e < heads;
+        const int i = it.r.i0 + qi;
+        tl.row[c] = there ? (it.s.row0 + i) * p.h_q + kv_head * p.group + head0 + e : -1;
+        tl.last[c] = !there ? -1 : (p.causal ? min(it.s.kv - 1, shift + i) : it.s.kv - 1);
+        tl.first[c] = there && p.window >= 0 ? shift + i - p.window : 0;
+        tl.neg_m[c] = 0.f;
+        tl.limit[c] = -CUDART_INF_F;
+    }
+#pragma unroll
+    for (int k = 0; k < S::kCols / 8; ++k) {
+        const int c = c0 + k * 8 + (r >> 4), part = r & 15;
+        const int qi = c / p.heads_per_tile, e = c - qi * p.heads_per_tile;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (qi < queries && e < heads)
+            w = reinterpret_cast<const uint4*>(
+                p.q + static_cast<long long>(it.s.row0 + it.r.i0 + qi) * p.q_stride +
+                (kv_head * p.group + head0 + e) * kHeadDim)[part];
+        if constexpr (kE) {
+            float x[8];
+            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[i] = __uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
+                top = fmaxf(top, fabsf(x[i]));
+            }
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            // 2^(7 - e) for a largest element in [2^e, 2^(e+1)).
+            const int ex = min(max(static_cast<int>(__float_as_uint(top) >> 23), 20), 250);
+            const float up = __uint_as_float(static_cast<uint32_t>(261 - ex) << 23);
+            if (part == 0) tl.qf[c] = __uint_as_float(static_cast<uint32_t>(ex - 7) << 23);
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float y[4], z[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = x[4 * i + j] * up;
+                hi[i] = ptx::pack_e4m3x4(y[0], y[1], y[2], y[3]);
+                e4m3x4_to_float(hi[i], z);
+                lo[i] = ptx::pack_e4m3x4(y[0] - z[0], y[1] - z[1], y[2] - z[2], y[3] - z[3]);
+            }
+            uint8_t* at = sq + c * 128 + (((part >> 1) ^ (c & 7)) << 4) + (part & 1) * 8;
+            *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(at + S::kQPiece) = make_uint2(lo[0], lo[1]);
+        } else {
+            *reinterpret_cast<uint4*>(sq + (part >> 3) * S::kN * 128 + c * 128 +
+                                      (((part & 7) ^ (c & 7)) << 4)) = w;
+        }
+    }
+}
+
+// A thread's weights of kSub columns into its row of P.
+template <bool kE, int kR>
+__device__ __forceinline__ void store_weights(const float (&w)[Shape<kE, kR>::kSub], uint32_t row,
+                                              int x, int c, uint32_t keep) {
+    using S = Shape<kE, kR>;
+    auto at = [&](int byte) -> uint32_t {  // byte of the row (both buffers), swizzled
+        return row + (byte >> 7) * S::kPBuf + ((((byte & 127) >> 4) ^ x) << 4) + (byte & 15);
+    };
+    if constexpr (kE) {
+        uint32_t piece[3][S::kSub / 4];
+#pragma unroll
+        for (int i = 0; i < S::kSub / 4; ++i) {
+            uint32_t hi[2], mid[2], lo[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const __half2 h = __floats2half2_rn(w[4 * i + 2 * j], w[4 * i + 2 * j + 1]);
+                const uint32_t v = *reinterpret_cast<const uint32_t*>(&h) & keep;
+                hi[j] = v & 0xff00ff00u;
+                const uint32_t rest = hsub2(v, hi[j]);
+                mid[j] = rest & 0xff00ff00u;
+                // The last piece is rounded (half of its last place added).
+                lo[j] = hsub2(rest, mid[j]) + 0x00800080u;
+            }
+            piece[0][i] = prmt(hi[0], hi[1], 0x7531);
+            piece[1][i] = prmt(mid[0], mid[1], 0x7531);
+            piece[2][i] = prmt(lo[0], lo[1], 0x7531);
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int byte = (S::p_offset(i) >= S::kPBuf ? 128 + S::p_offset(i) - S::kPBuf
+                                                         : S::p_offset(i)) + c;
+            if constexpr (S::kSub == 16)
+                ptx::st_shared_v4(at(byte), piece[i][0], piece[i][1], piece[i][2], piece[i][3]);
+            else
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at(byte)),
+                             "r"(piece[i][0]), "r"(piece[i][1])
+                             : "memory");
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < S::kSub / 8; ++i)
+            ptx::st_shared_v4(at(2 * c + 16 * i), ptx::pack_bf16x2(w[8 * i], w[8 * i + 1]),
+                              ptx::pack_bf16x2(w[8 * i + 2], w[8 * i + 3]),
+                              ptx::pack_bf16x2(w[8 * i + 4], w[8 * i + 5]),
+                              ptx::pack_bf16x2(w[8 * i + 6], w[8 * i + 7]));
+    }
+}
+
+// Four warps and kCols columns: thread r holds key r of the tile, and Tensor
+// Memory lane r.  A wait that gives up sets `dead`: the warp then goes through
+// its tiles without waiting (it keeps the group's barriers in step) and the
+// results are unspecified.
+template <bool kE, int kR>
+__device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, uint8_t* sq,
+                                             uint32_t sp, uint8_t* ring, uint32_t tmem,
+                                             const WaitCtx& wc, int group) {
+    using S = Shape<kE, kR>;
+    constexpr int kCols = S::kCols, kSub = S::kSub;
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
+    const int r = quarter * 32 + lane;
+    const int c0 = group * kCols;
+    const int bar_id = 1 + group;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_tm = tmem + lanes + c0, o_tm = tmem + lanes + 2 * S::kN + c0;
+    const uint32_t p_row = sp + r * 128;
+    constexpr float kBias = kE ? kBiasE4M3 : 0.f;
+    uint32_t g = 0, used = 0;
+    bool dead = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!dead && !wait_bar_warp(ptx::smem_u32(bar), parity, wc)) dead = true;
+    };
+
+    Cursor c = tl.cursor;
+    bool tail_part = false;
+    while (c.left > 0) {
+        const Item it = cursor_item(p, c);
+        load_rows<kE, kR>(p, tl, sq, it, c.h, c0, r);
+        ptx::fence_proxy_async_smem();
+        group_sync(bar_id);
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&tl.q_full));
+
+        const int head = c.h / p.head_tiles;
+        const int* table = p.table + static_cast<long long>(c.b) * p.max_pages;
+        const int shift = it.s.len - it.s.n;
+        const int min_last = p.causal ? min(it.s.kv - 1, shift + it.r.i0) : it.s.kv - 1;
+        const int max_first = p.window >= 0 ? shift + it.r.i1 - p.window : 0;
+        // Scales of this thread's key: the page one tile ahead, its scales in flight.
+        auto page_of = [&](int tile) -> int {
+            const int key = (it.r.tile0 + c.j + tile) * 128 + r;
+            return key < it.r.end ? table[p.div_page.div(key)] : -1;
+        };
+        float ks = 0.f, vs = 0.f, ks_next = 0.f, vs_next = 0.f;
+        int page_next = -1;
+        auto scales_of = [&](int page, float& a, float& b) {
+            a = b = 0.f;
+            if (page >= 0 && page < p.num_pages) {
+                const long long at = static_cast<long long>(page) * p.h_kv + head;
+                a = p.k_scale[at];
+                b = p.v_scale[at];
+            }
+        };
+        if constexpr (kE) {
+            const int page = page_of(0);
+            page_next = it.m > 1 ? page_of(1) : -1;
+            scales_of(page, ks_next, vs_next);
+        }
+        float l[kCols];
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) l[i] = 0.f;
+
+        for (int j = 0; j < it.m; ++j, ++g) {
+            float kc = p.scale_log2, lv = 0.f, inv_vs = 1.f;
+            uint32_t keep = 0xffffffffu;
+            if constexpr (kE) {
+                ks = ks_next;
+                vs = vs_next;
+                scales_of(page_next, ks_next, vs_next);
+                page_next = j + 2 < it.m ? page_of(j + 2) : -1;
+                kc *= ks;
+                lv = fminf(fmaxf(__log2f(vs), -64.f), 64.f);
+                if (!(vs >= 0x1p-64f)) keep = 0;  // V is taken as zero; its weight stays in l
+                inv_vs = ptx::ex2(-lv);
+            }
+            const int key0 = (it.r.tile0 + c.j + j) * 128, key = key0 + r;
+            const bool masked = key0 + 127 > min_last || key0 < max_first;
+            // V's tile in the ring: K0, then K(j+1), V(j) in turn.
+            const uint32_t v_used = used + (j + 1 < it.m ? 2 * j + 2 : 2 * it.m - 1);
+
+            wait(&tl.s_full[g & 1], (g >> 1) & 1);
+            ptx::tc_fence_after();
+            float y[kCols];
+#pragma unroll
+            for (int b = 0; b < kCols / kSub; ++b) {
+                float x[kSub];
+                tmem_load(s_tm + (g & 1) * S::kN + b * kSub, x);
+#pragma unroll
+                for (int i = 0; i < kSub; ++i) y[b * kSub + i] = x[i];
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&tl.s_free[g & 1]));
+
+            bool over = false;
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) {
+                if constexpr (kE) y[i] = fmaf(y[i] * tl.qf[c0 + i], kc, lv);
+                else y[i] *= kc;
+                if (masked && (key > tl.last[c0 + i] || key < tl.first[c0 + i]))
+                    y[i] = -CUDART_INF_F;
+                over |= y[i] > tl.limit[c0 + i];
+            }
+            if (group_any(bar_id, over)) {
+                // Some weight would pass 2^kSlack: raise the rows' units.
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) {
+                    float m = y[i];
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1)
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    if (lane == 0) tl.wmax[quarter][c0 + i] = m;
+                }
+                group_sync(bar_id);
+                if (j > 0) {
+                    wait(&tl.pv_done, (g - 1) & 1);
+                    ptx::tc_fence_after();
+                }
+#pragma unroll
+                for (int b = 0; b < kCols / kSub; ++b) {
+                    float o[kSub];
+                    if (j > 0) tmem_load(o_tm + b * kSub, o);
+#pragma unroll
+                    for (int i = 0; i < kSub; ++i) {
+                        const int col = c0 + b * kSub + i;
+                        const float m = fmaxf(fmaxf(tl.wmax[0][col], tl.wmax[1][col]),
+                                              fmaxf(tl.wmax[2][col], tl.wmax[3][col]));
+                        const bool fresh = tl.limit[col] == -CUDART_INF_F;
+                        const float old = -tl.neg_m[col] + kBias;
+                        const float want = ceilf(m);
+                        const float alpha = fresh ? 0.f : ptx::ex2(fminf(old - want, 0.f));
+                        l[b * kSub + i] *= alpha;
+                        if (j > 0) o[i] *= alpha;
+                    }
+                    if (j > 0) tmem_store(o_tm + b * kSub, o);
+                }
+                if (j > 0) {
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before();
+                }
+                group_sync(bar_id);
+                if (r < kCols) {
+                    const int col = c0 + r;
+                    const float m = fmaxf(fmaxf(tl.wmax[0][col], tl.wmax[1][col]),
+                                          fmaxf(tl.wmax[2][col], tl.wmax[3][col]));
+                    const bool fresh = tl.limit[col] == -CUDART_INF_F;
+                    const float old = -tl.neg_m[col] + kBias;
+                    float want = ceilf(m);
+                    if (!fresh) want = fmaxf(want, old);
+                    if (m > -CUDART_INF_F) {
+                        tl.neg_m[col] = kBias - want;
+                        tl.limit[col] = want + kSlack;
+                    }
+                }
+                group_sync(bar_id);
+            }
+            // The products that read P last must be done.
+            if (g > 0) wait(&tl.pv_done, (g - 1) & 1);
+#pragma unroll
+            for (int b = 0; b < kCols / kSub; ++b) {
+                float w[kSub];
+#pragma unroll
+                for (int i = 0; i < kSub; ++i) {
+                    w[i] = ptx::ex2(y[b * kSub + i] + tl.neg_m[c0 + b * kSub + i]);
+                    l[b * kSub + i] = fmaf(w[i], inv_vs, l[b * kSub + i]);
+                }
+                store_weights<kE, kR>(w, p_row, r & 7, c0 + b * kSub, keep);
+            }
+            if (key0 + 127 >= it.r.end) {
+                // Slots past the end hold anything: zero them before 0 * NaN.
+                wait(&tl.full[v_used % S::kSlots], (v_used / S::kSlots) & 1);
+                if (key >= it.r.end && group == 0) {
+                    uint4* row = reinterpret_cast<uint4*>(ring + (v_used % S::kSlots) * S::kTile +
+                                                          r * 128);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        row[i] = make_uint4(0, 0, 0, 0);
+                        if constexpr (!kE) row[1024 + i] = make_uint4(0, 0, 0, 0);
+                    }
+                }
+            }
+            ptx::fence_proxy_async_smem();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&tl.p_full));
+        }
+        used += 2 * it.m;
+
+        // The item's result, or the share's part of it.
+        const float mine = lane_sums<kCols>(l, lane);
+        if (lane < kCols) tl.wmax[quarter][c0 + lane] = mine;
+        wait(&tl.pv_done, (g - 1) & 1);
+        ptx::tc_fence_after();
+        group_sync(bar_id);
+        const bool whole = c.j == 0 && it.m == it.r.n;
+        const long long slot = static_cast<long long>(blockIdx.x) * 2 + (c.j == 0 ? 1 : 0);
+        if (r < kCols) {
+            const int col = c0 + r;
+            const float sum = (tl.wmax[0][col] + tl.wmax[1][col]) +
+                              (tl.wmax[2][col] + tl.wmax[3][col]);
+            const int row = tl.row[col];
+            if (whole) {
+                if (row >= 0) {
+                    const int q = row / p.h_q;
+                    p.lse[static_cast<long long>(row - q * p.h_q) * p.total_q + q] =
+                        sum > 0.f ? (log2f(sum) - tl.neg_m[col]) * 0.69314718055994531f
+                                  : -CUDART_INF_F;
+                }
+                tl.limit[col] = sum > 0.f ? 1.f / sum : 0.f;
+            } else {
+                p.part_ml[slot * kR + col] = make_float2(-tl.neg_m[col], sum);
+            }
+        }
+        group_sync(bar_id);
+#pragma unroll
+        for (int b = 0; b < kCols / kSub; ++b) {
+            float o[kSub];
+            tmem_load(o_tm + b * kSub, o);
+#pragma unroll
+            for (int i = 0; i < kSub; ++i) {
+                const int col = c0 + b * kSub + i;
+                if (whole) {
+                    const int row = tl.row[col];
+                    if (row >= 0)
+                        p.o[static_cast<long long>(row) * kHeadDim + r] =
+                            __float2bfloat16_rn(o[i] * tl.limit[col]);
+                } else {
+                    p.part_o[(slot * kR + col) * kHeadDim + r] = o[i];
+                }
+            }
+        }
+        ptx::tc_fence_before();
+        if (!whole && c.j == 0) {
+            // It begins here and goes on in the next shares.
+            tail_part = true;
+            if (threadIdx.x == 0) {
+                const int head0 = (c.h % p.head_tiles) * p.heads_per_tile;
+                const long long last = tl.begin + tl.chunk - it.m + it.r.n - 1;
+                p.meta[blockIdx.x] =
+                    make_int4(static_cast<int>(last / tl.chunk - blockIdx.x) + 1,
+                              it.s.row0 + it.r.i0, head * p.group + head0,
+                              (it.r.i1 - it.r.i0 + 1) |
+                                  (min(p.heads_per_tile, p.group - head0) << 16));
+            }
+        }
+        group_sync(bar_id);  // the rows' arrays are free for the next item
+        cursor_next(p, c, it);
+    }
+    if (threadIdx.x == 0 && !tail_part) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+}
+
+template <bool kE, int kR>
+__global__ void __launch_bounds__(Shape<kE, kR>::kThreads, Shape<kE, kR>::kCtasPerSm)
+    attn_fwd_cache_kernel(const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v,
+                          const __grid_constant__ FwdCacheParams p) {
+    using S = Shape<kE, kR>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = ptx::smem_u32(smem);
+    Tail& tl = *reinterpret_cast<Tail*>(smem + S::kOffTail);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kSoftWarps = S::kSoftThreads / 32;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kSlots; ++i) {
+            ptx::mbar_init(ptx::smem_u32(&tl.full[i]), 1);
+            ptx::mbar_init(ptx::smem_u32(&tl.empty[i]), 1);
+        }
+        ptx::mbar_init(ptx::smem_u32(&tl.q_full), kSoftWarps);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(ptx::smem_u32(&tl.s_full[i]), 1);
+            ptx::mbar_init(ptx::smem_u32(&tl.s_free[i]), kSoftWarps);
+        }
+        ptx::mbar_init(ptx::smem_u32(&tl.p_full), kSoftWarps);
+        ptx::mbar_init(ptx::smem_u32(&tl.pv_done), 1);
+        ptx::mbar_init(ptx::smem_u32(&tl.drain), 1);
+        tl.abort = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&tm_k);
+        ptx::prefetch_tmap(&tm_v);
+    }
+    if (warp == kSoftWarps) {
+        ptx::tmem_alloc(ptx::smem_u32(&tl.tmem), S::kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = tl.tmem;
+    const WaitCtx wc{&tl.abort, p.status, p.timeout_ns};
+
+    // All that came before on the stream is done and visible from here on.
+    grid_wait();
+    grid_launch_dependents();
+    find_share<S::kThreads>(p, tl);
+
+    if (warp < kSoftWarps)
+        softmax_role<kE, kR>(p, tl, smem + S::kOffQ, sbase + S::kOffP, smem + S::kOffRing, tmem,
+                             wc, warp >> 2);
+    else if (warp == kSoftWarps)
+        mma_role<kE, kR>(p, tl, sbase + S::kOffQ, sbase + S::kOffP, sbase + S::kOffRing, tmem, wc);
+    else
+        producer_role<kE, kR>(p, &tm_k, &tm_v, tl, sbase + S::kOffRing, wc, lane);
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == kSoftWarps) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, S::kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------ merge
+// The parts of the items that a share's border cuts.  Block (c, y): the item
+// that begins in share c and goes on, rows y, y + 8, ...; a warp takes every
+// eighth part, and the warps' sums are joined in order.
+//     O = sum_i 2^(u_i - U) acc_i / sum_i 2^(u_i - U) l_i,   U = max u_i.
+constexpr int kMergeWarps = 8;
+template <int kR>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    attn_cache_merge_kernel(const __grid_constant__ FwdCacheParams p) {
+    grid_wait();
+    const int4 meta = p.meta[blockIdx.x];
+    const int parts = meta.x;
+    if (parts <= 0) return;
+    const int queries = meta.w & 0xffff, heads = meta.w >> 16;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ float4 acc_s[kMergeWarps][32];
+    __shared__ float2 ml_s[kMergeWarps];
+    for (int c = blockIdx.y; c < kR; c += gridDim.y) {
+        const int qi = c / p.heads_per_tile, e = c - qi * p.heads_per_tile;
+        if (qi >= queries || e >= heads) continue;  // the same for the whole block
+        auto slot = [&](int i) -> long long {
+            return (static_cast<long long>(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * kR + c;
+        };
+        float u = -CUDART_INF_F;
+        for (int i = lane; i < parts; i += 32) {
+            const float2 ml = p.part_ml[slot(i)];
+            if (ml.y > 0.f) u = fmaxf(u, ml.x);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, o));
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+        if (u > -CUDART_INF_F) {
+#pragma unroll 4
+            for (int i = warp; i < parts; i += kMergeWarps) {
+                const float2 ml = p.part_ml[slot(i)];
+                const float4 x =
+                    reinterpret_cast<const float4*>(p.part_o + slot(i) * kHeadDim)[lane];
+                const float a = ml.y > 0.f ? exp2f(ml.x - u) : 0.f;
+                l = fmaf(a, ml.y, l);
+                acc.x = fmaf(a, x.x, acc.x);
+                acc.y = fmaf(a, x.y, acc.y);
+                acc.z = fmaf(a, x.z, acc.z);
+                acc.w = fmaf(a, x.w, acc.w);
+            }
+        }
+        acc_s[warp][lane] = acc;
+        if (lane == 0) ml_s[warp].y = l;
+        __syncthreads();
+        if (warp == 0) {
+            for (int w = 1; w < kMergeWarps; ++w) {
+                const float4 x = acc_s[w][lane];
+                acc.x += x.x;
+                acc.y += x.y;
+                acc.z += x.z;
+                acc.w += x.w;
+                l += ml_s[w].y;
+            }
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const int q = meta.y + qi, h = meta.z + e;
+            reinterpret_cast<uint2*>(p.o + (static_cast<long long>(q) * p.h_q + h) * kHeadDim)[lane] =
+                make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv),
+                           ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
+            if (lane == 0)
+                p.lse[static_cast<long long>(h) * p.total_q + q] =
+                    l > 0.f ? (log2f(l) + u) * 0.69314718055994531f : -CUDART_INF_F;
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace cache
+}  // namespace sdpa10
