@@ -307,6 +307,7 @@ extern "C" int attn_fwd_cache(const attn_cache_t* c, const void* q, void* o, flo
     p.num_pages = c->num_pages;
     p.page_size = c->page_size;
     p.div_page = FastDiv::make(static_cast<uint32_t>(c->page_size));
+    p.div_heads = FastDiv::make(static_cast<uint32_t>(p.heads_per_tile));
     CUtensorMap tk, tv;
     if (!encode_pool(&tk, c, c->k_pages, p.box) || !encode_pool(&tv, c, c->v_pages, p.box))
         return ATTN_ERR_CUDA;

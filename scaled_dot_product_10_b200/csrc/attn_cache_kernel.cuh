@@ -40,9 +40,12 @@ namespace sdpa10 {
 namespace cache {
 
 constexpr int kMaxRows = 64;       // query rows of the widest tile
-constexpr int kMinChunk = 1;       // least key tiles of a CTA's share
-constexpr float kSlack = 4.f;      // log2 of the largest weight over 2^M
-constexpr float kBiasE4M3 = 11.f;  // weights are kept as 2^11 p: below 2^15 in FP16 and E5M2
+// log2 of a row's unit of weights, and of how far a weight may pass it before
+// the unit is raised.  E4M3 pages: 2^11 p stays below 2^15 in FP16 and E5M2,
+// and the smallest E5M2 number is 2^-27 of the unit.
+template <bool kE> constexpr float kBias = kE ? 11.f : 0.f;
+template <bool kE> constexpr float kSlack = kE ? 4.f : 8.f;
+constexpr float kFresh = 1e30f;  // offset of a row that has seen no key
 
 struct FwdCacheParams {
     const __nv_bfloat16* q;
@@ -56,7 +59,7 @@ struct FwdCacheParams {
     long long q_stride;
     int batch, max_pages, total_q, max_seqlen_q, n_uniform;
     int h_q, h_kv, group, num_pages, page_size;
-    FastDiv div_page;
+    FastDiv div_page, div_heads;  // page_size, heads_per_tile
     int box;             // keys of one TMA copy: the power of two that divides page_size, <= 128
     int heads_per_tile;  // query heads of a row tile
     int q_per_tile;      // queries of a row tile
@@ -175,7 +178,7 @@ __device__ __forceinline__ void mma_f8_warp(uint32_t d, uint64_t a, uint64_t b, 
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
 }
 
-// 32 lanes x 8 or 16 consecutive columns.
+// 32 lanes x 8, 16 or 32 consecutive columns.
 __device__ __forceinline__ void tmem_load(uint32_t t, float (&r)[8]) {
     uint32_t u[8];
     asm volatile(
@@ -200,6 +203,13 @@ __device__ __forceinline__ void tmem_load(uint32_t t, float (&r)[16]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) r[i] = __uint_as_float(u[i]);
 }
+__device__ __forceinline__ void tmem_load(uint32_t t, float (&r)[32]) {
+    uint32_t u[32];
+    ptx::tmem_ld32(t, u);
+    ptx::tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) r[i] = __uint_as_float(u[i]);
+}
 __device__ __forceinline__ void tmem_store(uint32_t t, const float (&r)[8]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t),
@@ -208,15 +218,12 @@ __device__ __forceinline__ void tmem_store(uint32_t t, const float (&r)[8]) {
         "r"(__float_as_uint(r[6])), "r"(__float_as_uint(r[7]))
         : "memory");
 }
-__device__ __forceinline__ void tmem_store(uint32_t t, const float (&r)[16]) {
-    float a[8], b[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        a[i] = r[i];
-        b[i] = r[8 + i];
-    }
-    tmem_store(t, a);
-    tmem_store(t + 8, b);
+
+// Maximum over the warp's lanes.
+__device__ __forceinline__ float warp_max(float x) {
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+    return m;
 }
 
 // Barrier of 128 threads that also tells whether any of them says yes.
@@ -269,7 +276,7 @@ struct Shape {
     static constexpr int kOffQ = 0;
     static constexpr int kOffP = kOffQ + (kQPieces * kQPiece + 1023) / 1024 * 1024;
     static constexpr int kOffRing = kOffP + kPBytes;
-    static constexpr int kTail = 3072;  // barriers and the small arrays below
+    static constexpr int kTail = 4608;  // barriers and the small arrays below
     // Two CTAs of an SM overlap one's softmax with the other's products.  Ring
     // and P of BF16 pages leave room for one, whose deeper ring has the same
     // bytes in flight.
@@ -279,31 +286,42 @@ struct Shape {
     static_assert(kSlots >= 3 && kSlots <= 8, "the ring needs K(j+1) beside K(j) and V(j)");
     static constexpr int kOffTail = kOffRing + kSlots * kTile;
     static constexpr int kAlloc = kOffTail + kTail + 1024;
-    static constexpr uint32_t kTmemCols = 3 * kN <= 64 ? 64 : (3 * kN <= 128 ? 128 : 256);
+    // The pieces of P side by side are one product of 3 kN columns, of which
+    // the epilogue adds three (an MMA of N columns takes 32 + N / 4 cycles here,
+    // N = 16 38, so four of 48 columns take 174 where twelve of 16 take 460);
+    // 64 rows leave no Tensor Memory for that and add up in place.
+    static constexpr bool kSideBySide = kE && kN <= 32;
+    static constexpr int kPN = kSideBySide ? 3 * kN : kN;  // columns of one product with V
+    static constexpr int kCols0 = 2 * kN + kPN;
+    static constexpr uint32_t kTmemCols = kCols0 <= 64 ? 64 : (kCols0 <= 128 ? 128 : 256);
     __host__ __device__ static constexpr int p_offset(int piece) {
         const int at = piece * kN * kElem;
         return at + kN * kElem <= 128 ? at : kPBuf + at - 128;
     }
 };
 
+struct __align__(16) Rows {
+    float scale[kMaxRows];   // of the row's scores: scale log2(e), E4M3: times 2^-e of its Q
+    float offset[kMaxRows];  // bias - M of the row, kFresh while it has seen no key
+    int last[kMaxRows];      // last key the row sees
+    int first[kMaxRows];     // first one
+    int row[kMaxRows];       // query * h_q + head; -1: no such row
+};
+
 struct Tail {
+    Rows rows[2];  // of this item and the next
+    float wmax[4][kMaxRows];
+    float alpha[kMaxRows];
     uint64_t full[8], empty[8];
     uint64_t q_full, s_full[2], s_free[2], p_full, pv_done, drain;
+    long long begin;  // first unit of this share
+    long long wsum[16];
     uint32_t tmem;
     int abort;
     Cursor cursor;
-    int chunk;              // units of every share
-    long long begin;        // first unit of this one
-    long long wsum[16];
-    float qf[kMaxRows];     // E4M3: 2^-e of the row's scaling of Q
-    float neg_m[kMaxRows];  // minus log2 of the row's unit of weights
-    float limit[kMaxRows];  // largest y that leaves the unit as it is; -inf: no key seen yet
-    float wmax[4][kMaxRows];
-    int last[kMaxRows];     // last key the row sees
-    int first[kMaxRows];    // first one
-    int row[kMaxRows];      // query * h_q + head; -1: no such row
+    int chunk;  // units of every share
 };
-static_assert(sizeof(Tail) <= 3072, "");
+static_assert(sizeof(Tail) <= 4608, "");
 
 // Where this CTA's share of the units begins (every thread of the CTA calls).
 template <int kThreads>
@@ -311,18 +329,29 @@ __device__ __forceinline__ void find_share(const FwdCacheParams& p, Tail& tl) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per_seq = p.h_kv * p.head_tiles;
     constexpr int kWarps = kThreads / 32;
-    long long mine = 0;
-    for (int b = tid; b < p.batch; b += kThreads) mine += seq_units(p, load_seq(p, b));
-    long long v = mine;
+    // Inclusive sum of v over the CTA's threads; `all` is the whole sum.
+    auto scan = [&](long long v, long long& all) -> long long {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane == 0) tl.wsum[warp] = v;
-    __syncthreads();
-    long long total = 0;
-    for (int w = 0; w < kWarps; ++w) total += tl.wsum[w];
-    total *= per_seq;
-    long long chunk = (total + gridDim.x - 1) / gridDim.x;
-    if (chunk < kMinChunk) chunk = kMinChunk;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += up;
+        }
+        if (lane == 31) tl.wsum[warp] = v;
+        __syncthreads();
+        all = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) v += tl.wsum[w];
+            all += tl.wsum[w];
+        }
+        return v;
+    };
+    long long own = 0, total = 0;
+    for (int b = tid; b < p.batch; b += kThreads) own += seq_units(p, load_seq(p, b));
+    long long inc = scan(own * per_seq, total);
+    const unsigned long long grid = gridDim.x;
+    const long long chunk = total >> 31 ? (total + grid - 1) / grid
+                                        : (static_cast<uint32_t>(total) + gridDim.x - 1) / gridDim.x;
     const long long begin = chunk * blockIdx.x;
     if (tid == 0) {
         const long long rest = total - begin;
@@ -330,48 +359,40 @@ __device__ __forceinline__ void find_share(const FwdCacheParams& p, Tail& tl) {
         tl.chunk = static_cast<int>(chunk);
         tl.begin = begin;
     }
-    if (begin >= total) {
-        __syncthreads();
-        return;
-    }
-    long long run = 0;
-    for (int base = 0; base < p.batch; base += kThreads) {
-        const int b = base + tid;
-        long long own = 0;
-        if (p.batch <= kThreads) own = mine;
-        else if (b < p.batch) own = seq_units(p, load_seq(p, b));
-        long long inc = own * per_seq;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long up = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += up;
-        }
-        __syncthreads();  // the sums of the pass before have been read
-        if (lane == 31) tl.wsum[warp] = inc;
-        __syncthreads();
-        long long all = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) inc += tl.wsum[w];
-            all += tl.wsum[w];
-        }
-        inc += run;
-        const long long exc = inc - own * per_seq;
-        if (begin >= exc && begin < inc) {
-            const long long rem = begin - exc;
-            const Seq s = load_seq(p, b);
-            int left = static_cast<int>(rem % own), t = 0;
-            for (;; ++t) {
-                const int n = row_tile(p, s, t).n;
-                if (left < n) break;
-                left -= n;
+    if (begin < total) {
+        long long run = 0;
+        for (int base = 0; base < p.batch; base += kThreads) {
+            const int b = base + tid;
+            if (p.batch > kThreads) {  // more sequences than threads: again, in passes
+                __syncthreads();
+                own = b < p.batch ? seq_units(p, load_seq(p, b)) : 0;
+                long long all;
+                inc = scan(own * per_seq, all) + run;
+                run += all;
             }
-            tl.cursor.b = b;
-            tl.cursor.h = static_cast<int>(rem / own);
-            tl.cursor.t = t;
-            tl.cursor.j = left;
+            const long long exc = inc - own * per_seq;
+            if (begin >= exc && begin < inc) {
+                const long long rem = begin - exc;
+                const Seq s = load_seq(p, b);
+                int left, t = 0;
+                if (rem >> 31) {
+                    tl.cursor.h = static_cast<int>(rem / own);
+                    left = static_cast<int>(rem % own);
+                } else {
+                    tl.cursor.h = static_cast<int>(rem) / static_cast<int>(own);
+                    left = static_cast<int>(rem) % static_cast<int>(own);
+                }
+                for (;; ++t) {
+                    const int n = row_tile(p, s, t).n;
+                    if (left < n) break;
+                    left -= n;
+                }
+                tl.cursor.b = b;
+                tl.cursor.t = t;
+                tl.cursor.j = left;
+            }
+            if (p.batch > kThreads && run > begin) break;  // the same for every thread
         }
-        run += all;
-        if (run > begin) break;  // the same for every thread
     }
     __syncthreads();
 }
@@ -445,8 +466,8 @@ __device__ __forceinline__ void mma_role(const FwdCacheParams& p, Tail& tl, uint
     // A = K or V^T (128 rows), B = Q or P (kN rows); P's pieces are E5M2 (code 1).
     constexpr uint32_t kIdQK =
         kE ? idesc_e4m3_f32(128, S::kN, 0, 0) : idesc_bf16_f32(128, S::kN, 0, 0);
-    constexpr uint32_t kIdPV = kE ? idesc_e4m3_f32(128, S::kN, 1, 1) | (1u << 10)
-                                  : idesc_bf16_f32(128, S::kN, 1, 1);
+    constexpr uint32_t kIdPV = kE ? idesc_e4m3_f32(128, S::kPN, 1, 1) | (1u << 10)
+                                  : idesc_bf16_f32(128, S::kPN, 1, 1);
     const uint32_t o_tm = tmem + 2 * S::kN;
     uint32_t used = 0;   // ring tiles taken
     uint32_t g = 0;      // score tiles issued
@@ -497,7 +518,7 @@ __device__ __forceinline__ void mma_role(const FwdCacheParams& p, Tail& tl, uint
             desc_lo_sw128(ring + (used % S::kSlots) * S::kTile, kE ? S::kTile : 16384);
         constexpr int kSteps = kE ? 4 : 8, kStepBytes = kE ? 4096 : 2048;
 #pragma unroll
-        for (int i = 0; i < S::kPPieces; ++i)
+        for (int i = 0; i < (S::kSideBySide ? 1 : S::kPPieces); ++i)
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
                 const uint64_t a = desc_from_lo(va + ((k * kStepBytes) >> 4));
@@ -555,37 +576,41 @@ __device__ __forceinline__ float lane_sums(float (&v)[kC], int lane) {
 // The queries of an item's rows [c0, c0 + kCols) into shared memory, and what
 // the rows see.  128 threads.
 template <bool kE, int kR>
-__device__ __forceinline__ void load_rows(const FwdCacheParams& p, Tail& tl, uint8_t* sq,
+__device__ __forceinline__ void load_rows(const FwdCacheParams& p, Rows& rows, uint8_t* sq,
                                           const Item& it, int h, int c0, int r) {
     using S = Shape<kE, kR>;
-    const int head0 = (h % p.head_tiles) * p.heads_per_tile;  // in the group
-    const int heads = min(p.heads_per_tile, p.group - head0);
     const int kv_head = h / p.head_tiles;
+    const int head0 = (h - kv_head * p.head_tiles) * p.heads_per_tile;  // in the group
+    const int heads = min(p.heads_per_tile, p.group - head0);
     const int queries = it.r.i1 - it.r.i0 + 1;
     const int shift = it.s.len - it.s.n;
+    uint4 w[S::kCols / 8];
+#pragma unroll
+    for (int k = 0; k < S::kCols / 8; ++k) {
+        const int c = c0 + k * 8 + (r >> 4);
+        const int qi = p.div_heads.div(c), e = c - qi * p.heads_per_tile;
+        w[k] = make_uint4(0, 0, 0, 0);
+        if (qi < queries && e < heads)
+            w[k] = reinterpret_cast<const uint4*>(
+                p.q + static_cast<long long>(it.s.row0 + it.r.i0 + qi) * p.q_stride +
+                (kv_head * p.group + head0 + e) * kHeadDim)[r & 15];
+    }
     if (r < S::kCols) {
         const int c = c0 + r;
-        const int qi = c / p.heads_per_tile, e = c - qi * p.heads_per_tile;
+        const int qi = p.div_heads.div(c), e = c - qi * p.heads_per_tile;
         const bool there = qi < queries && e < heads;
         const int i = it.r.i0 + qi;
-        tl.row[c] = there ? (it.s.row0 + i) * p.h_q + kv_head * p.group + head0 + e : -1;
-        tl.last[c] = !there ? -1 : (p.causal ? min(it.s.kv - 1, shift + i) : it.s.kv - 1);
-        tl.first[c] = there && p.window >= 0 ? shift + i - p.window : 0;
-        tl.neg_m[c] = 0.f;
-        tl.limit[c] = -CUDART_INF_F;
+        rows.row[c] = there ? (it.s.row0 + i) * p.h_q + kv_head * p.group + head0 + e : -1;
+        rows.last[c] = !there ? -1 : (p.causal ? min(it.s.kv - 1, shift + i) : it.s.kv - 1);
+        rows.first[c] = there && p.window >= 0 ? shift + i - p.window : 0;
+        rows.offset[c] = kFresh;
     }
 #pragma unroll
     for (int k = 0; k < S::kCols / 8; ++k) {
         const int c = c0 + k * 8 + (r >> 4), part = r & 15;
-        const int qi = c / p.heads_per_tile, e = c - qi * p.heads_per_tile;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (qi < queries && e < heads)
-            w = reinterpret_cast<const uint4*>(
-                p.q + static_cast<long long>(it.s.row0 + it.r.i0 + qi) * p.q_stride +
-                (kv_head * p.group + head0 + e) * kHeadDim)[part];
         if constexpr (kE) {
             float x[8];
-            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+            const uint32_t v[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
             float top = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -597,7 +622,9 @@ __device__ __forceinline__ void load_rows(const FwdCacheParams& p, Tail& tl, uin
             // 2^(7 - e) for a largest element in [2^e, 2^(e+1)).
             const int ex = min(max(static_cast<int>(__float_as_uint(top) >> 23), 20), 250);
             const float up = __uint_as_float(static_cast<uint32_t>(261 - ex) << 23);
-            if (part == 0) tl.qf[c] = __uint_as_float(static_cast<uint32_t>(ex - 7) << 23);
+            if (part == 0)
+                rows.scale[c] =
+                    p.scale_log2 * __uint_as_float(static_cast<uint32_t>(ex - 7) << 23);
             uint32_t hi[2], lo[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -613,7 +640,7 @@ __device__ __forceinline__ void load_rows(const FwdCacheParams& p, Tail& tl, uin
             *reinterpret_cast<uint2*>(at + S::kQPiece) = make_uint2(lo[0], lo[1]);
         } else {
             *reinterpret_cast<uint4*>(sq + (part >> 3) * S::kN * 128 + c * 128 +
-                                      (((part & 7) ^ (c & 7)) << 4)) = w;
+                                      (((part & 7) ^ (c & 7)) << 4)) = w[k];
         }
     }
 }
@@ -621,7 +648,7 @@ __device__ __forceinline__ void load_rows(const FwdCacheParams& p, Tail& tl, uin
 // A thread's weights of kSub columns into its row of P.
 template <bool kE, int kR>
 __device__ __forceinline__ void store_weights(const float (&w)[Shape<kE, kR>::kSub], uint32_t row,
-                                              int x, int c, uint32_t keep) {
+                                              int x, int c) {
     using S = Shape<kE, kR>;
     auto at = [&](int byte) -> uint32_t {  // byte of the row (both buffers), swizzled
         return row + (byte >> 7) * S::kPBuf + ((((byte & 127) >> 4) ^ x) << 4) + (byte & 15);
@@ -634,7 +661,7 @@ __device__ __forceinline__ void store_weights(const float (&w)[Shape<kE, kR>::kS
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const __half2 h = __floats2half2_rn(w[4 * i + 2 * j], w[4 * i + 2 * j + 1]);
-                const uint32_t v = *reinterpret_cast<const uint32_t*>(&h) & keep;
+                const uint32_t v = *reinterpret_cast<const uint32_t*>(&h);
                 hi[j] = v & 0xff00ff00u;
                 const uint32_t rest = hsub2(v, hi[j]);
                 mid[j] = rest & 0xff00ff00u;
@@ -675,30 +702,35 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
                                              uint32_t sp, uint8_t* ring, uint32_t tmem,
                                              const WaitCtx& wc, int group) {
     using S = Shape<kE, kR>;
-    constexpr int kCols = S::kCols, kSub = S::kSub;
+    constexpr int kCols = S::kCols, kSub = S::kSub, kPairs = kCols / 2;
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
     const int r = quarter * 32 + lane;
-    const int c0 = group * kCols;
+    const int c0 = S::kGroups > 1 ? group * kCols : 0;
     const int bar_id = 1 + group;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_tm = tmem + lanes + c0, o_tm = tmem + lanes + 2 * S::kN + c0;
     const uint32_t p_row = sp + r * 128;
-    constexpr float kBias = kE ? kBiasE4M3 : 0.f;
-    uint32_t g = 0, used = 0;
+    uint32_t g = 0, used = 0, items = 0;
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (!dead && !wait_bar_warp(ptx::smem_u32(bar), parity, wc)) dead = true;
     };
-
-    Cursor c = tl.cursor;
-    bool tail_part = false;
-    while (c.left > 0) {
-        const Item it = cursor_item(p, c);
-        load_rows<kE, kR>(p, tl, sq, it, c.h, c0, r);
+    auto stage = [&](const Item& it, int h) {
+        load_rows<kE, kR>(p, tl.rows[items & 1], sq, it, h, c0, r);
         ptx::fence_proxy_async_smem();
         group_sync(bar_id);
         if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&tl.q_full));
+    };
 
+    Cursor c = tl.cursor;
+    bool tail_part = false;
+    Item it;
+    if (c.left > 0) {
+        it = cursor_item(p, c);
+        stage(it, c.h);
+    }
+    while (c.left > 0) {
+        Rows& rows = tl.rows[items & 1];
         const int head = c.h / p.head_tiles;
         const int* table = p.table + static_cast<long long>(c.b) * p.max_pages;
         const int shift = it.s.len - it.s.n;
@@ -709,7 +741,7 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
             const int key = (it.r.tile0 + c.j + tile) * 128 + r;
             return key < it.r.end ? table[p.div_page.div(key)] : -1;
         };
-        float ks = 0.f, vs = 0.f, ks_next = 0.f, vs_next = 0.f;
+        float ks_next = 0.f, vs_next = 0.f;
         int page_next = -1;
         auto scales_of = [&](int page, float& a, float& b) {
             a = b = 0.f;
@@ -724,60 +756,82 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
             page_next = it.m > 1 ? page_of(1) : -1;
             scales_of(page, ks_next, vs_next);
         }
-        float l[kCols];
+        uint64_t l[kPairs];
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) l[i] = 0.f;
+        for (int i = 0; i < kPairs; ++i) l[i] = 0;
 
         for (int j = 0; j < it.m; ++j, ++g) {
-            float kc = p.scale_log2, lv = 0.f, inv_vs = 1.f;
-            uint32_t keep = 0xffffffffu;
+            // Scores become exponents: x = S scale ks + log2(vs) + offset.
+            float ks = p.scale_log2, lv = 0.f, inv_vs = 1.f;
+            bool zero = false;
             if constexpr (kE) {
                 ks = ks_next;
-                vs = vs_next;
+                const float vs = vs_next;
                 scales_of(page_next, ks_next, vs_next);
                 page_next = j + 2 < it.m ? page_of(j + 2) : -1;
-                kc *= ks;
                 lv = fminf(fmaxf(__log2f(vs), -64.f), 64.f);
-                if (!(vs >= 0x1p-64f)) keep = 0;  // V is taken as zero; its weight stays in l
                 inv_vs = ptx::ex2(-lv);
+                zero = !(vs >= 0x1p-64f);  // V is taken as zero; its weight stays in l
             }
+            const uint64_t ks2 = ptx::f2_pack(ks, ks), lv2 = ptx::f2_pack(lv, lv);
             const int key0 = (it.r.tile0 + c.j + j) * 128, key = key0 + r;
             const bool masked = key0 + 127 > min_last || key0 < max_first;
-            // V's tile in the ring: K0, then K(j+1), V(j) in turn.
-            const uint32_t v_used = used + (j + 1 < it.m ? 2 * j + 2 : 2 * it.m - 1);
+            const uint32_t s_at = s_tm + (g & 1) * S::kN;
+            float x[kCols];
+            auto exponents = [&](bool absolute) {
+                tmem_load(s_at, x);
+#pragma unroll
+                for (int i = 0; i < kCols; i += 4) {
+                    const float4 o = absolute ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                              : *reinterpret_cast<const float4*>(&rows.offset[c0 + i]);
+                    uint64_t o2[2] = {ptx::f2_pack(o.x, o.y), ptx::f2_pack(o.z, o.w)};
+                    uint64_t x2[2] = {ptx::f2_pack(x[i], x[i + 1]), ptx::f2_pack(x[i + 2], x[i + 3])};
+                    if constexpr (kE) {
+                        const float4 q = *reinterpret_cast<const float4*>(&rows.scale[c0 + i]);
+                        x2[0] = ptx::f2_mul(x2[0], ptx::f2_pack(q.x, q.y));
+                        x2[1] = ptx::f2_mul(x2[1], ptx::f2_pack(q.z, q.w));
+                        o2[0] = ptx::f2_add(o2[0], lv2);
+                        o2[1] = ptx::f2_add(o2[1], lv2);
+                    }
+                    ptx::f2_unpack(ptx::f2_fma(x2[0], ks2, o2[0]), x[i], x[i + 1]);
+                    ptx::f2_unpack(ptx::f2_fma(x2[1], ks2, o2[1]), x[i + 2], x[i + 3]);
+                }
+                if (masked) {
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i)
+                        if (key > rows.last[c0 + i] || key < rows.first[c0 + i])
+                            x[i] = -CUDART_INF_F;
+                }
+            };
 
             wait(&tl.s_full[g & 1], (g >> 1) & 1);
             ptx::tc_fence_after();
-            float y[kCols];
+            exponents(false);
+            float top = x[0];
 #pragma unroll
-            for (int b = 0; b < kCols / kSub; ++b) {
-                float x[kSub];
-                tmem_load(s_tm + (g & 1) * S::kN + b * kSub, x);
-#pragma unroll
-                for (int i = 0; i < kSub; ++i) y[b * kSub + i] = x[i];
-            }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&tl.s_free[g & 1]));
-
-            bool over = false;
-#pragma unroll
-            for (int i = 0; i < kCols; ++i) {
-                if constexpr (kE) y[i] = fmaf(y[i] * tl.qf[c0 + i], kc, lv);
-                else y[i] *= kc;
-                if (masked && (key > tl.last[c0 + i] || key < tl.first[c0 + i]))
-                    y[i] = -CUDART_INF_F;
-                over |= y[i] > tl.limit[c0 + i];
-            }
-            if (group_any(bar_id, over)) {
-                // Some weight would pass 2^kSlack: raise the rows' units.
+            for (int i = 1; i + 1 < kCols; i += 2) top = ptx::max3(top, x[i], x[i + 1]);
+            top = fmaxf(top, x[kCols - 1]);
+            if (group_any(bar_id, top > kBias<kE> + kSlack<kE>)) {
+                // Some weight is too large for its row's unit: raise the units.
+                exponents(true);
+                float mine = 0.f;
 #pragma unroll
                 for (int i = 0; i < kCols; ++i) {
-                    float m = y[i];
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1)
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                    if (lane == 0) tl.wmax[quarter][c0 + i] = m;
+                    const float m = warp_max(x[i]);
+                    if (lane == i) mine = m;
+                }
+                if (lane < kCols) tl.wmax[quarter][c0 + lane] = mine;
+                group_sync(bar_id);
+                if (r < kCols) {
+                    const int col = c0 + r;
+                    const float m = fmaxf(fmaxf(tl.wmax[0][col], tl.wmax[1][col]),
+                                          fmaxf(tl.wmax[2][col], tl.wmax[3][col]));
+                    const float old = rows.offset[col];
+                    float off = old;
+                    if (m > -CUDART_INF_F) off = fminf(old, kBias<kE> - ceilf(m));
+                    rows.offset[col] = off;
+                    // 0 for a row's first keys, whose sums so far are 0.
+                    tl.alpha[col] = ptx::ex2(off - old);
                 }
                 group_sync(bar_id);
                 if (j > 0) {
@@ -785,57 +839,56 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
                     ptx::tc_fence_after();
                 }
 #pragma unroll
-                for (int b = 0; b < kCols / kSub; ++b) {
-                    float o[kSub];
-                    if (j > 0) tmem_load(o_tm + b * kSub, o);
+                for (int b = 0; b < kCols / 8; ++b) {
+                    float a[8];
 #pragma unroll
-                    for (int i = 0; i < kSub; ++i) {
-                        const int col = c0 + b * kSub + i;
-                        const float m = fmaxf(fmaxf(tl.wmax[0][col], tl.wmax[1][col]),
-                                              fmaxf(tl.wmax[2][col], tl.wmax[3][col]));
-                        const bool fresh = tl.limit[col] == -CUDART_INF_F;
-                        const float old = -tl.neg_m[col] + kBias;
-                        const float want = ceilf(m);
-                        const float alpha = fresh ? 0.f : ptx::ex2(fminf(old - want, 0.f));
-                        l[b * kSub + i] *= alpha;
-                        if (j > 0) o[i] *= alpha;
-                    }
-                    if (j > 0) tmem_store(o_tm + b * kSub, o);
-                }
-                if (j > 0) {
-                    ptx::tmem_wait_st();
-                    ptx::tc_fence_before();
-                }
-                group_sync(bar_id);
-                if (r < kCols) {
-                    const int col = c0 + r;
-                    const float m = fmaxf(fmaxf(tl.wmax[0][col], tl.wmax[1][col]),
-                                          fmaxf(tl.wmax[2][col], tl.wmax[3][col]));
-                    const bool fresh = tl.limit[col] == -CUDART_INF_F;
-                    const float old = -tl.neg_m[col] + kBias;
-                    float want = ceilf(m);
-                    if (!fresh) want = fmaxf(want, old);
-                    if (m > -CUDART_INF_F) {
-                        tl.neg_m[col] = kBias - want;
-                        tl.limit[col] = want + kSlack;
+                    for (int i = 0; i < 8; ++i) a[i] = tl.alpha[c0 + 8 * b + i];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        l[4 * b + i] = ptx::f2_mul(l[4 * b + i],
+                                                   ptx::f2_pack(a[2 * i], a[2 * i + 1]));
+                    if (j > 0) {
+#pragma unroll
+                        for (int i = 0; i < S::kPN / S::kN; ++i) {
+                            float o[8];
+                            tmem_load(o_tm + i * S::kN + 8 * b, o);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) o[k] *= a[k];
+                            tmem_store(o_tm + i * S::kN + 8 * b, o);
+                        }
                     }
                 }
-                group_sync(bar_id);
+                if (j > 0) ptx::tmem_wait_st();
+                exponents(false);
             }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&tl.s_free[g & 1]));
+
             // The products that read P last must be done.
             if (g > 0) wait(&tl.pv_done, (g - 1) & 1);
+            const uint64_t inv2 = ptx::f2_pack(inv_vs, inv_vs);
 #pragma unroll
             for (int b = 0; b < kCols / kSub; ++b) {
                 float w[kSub];
 #pragma unroll
-                for (int i = 0; i < kSub; ++i) {
-                    w[i] = ptx::ex2(y[b * kSub + i] + tl.neg_m[c0 + b * kSub + i]);
-                    l[b * kSub + i] = fmaf(w[i], inv_vs, l[b * kSub + i]);
+                for (int i = 0; i < kSub; i += 2) {
+                    w[i] = ptx::ex2(x[b * kSub + i]);
+                    w[i + 1] = ptx::ex2(x[b * kSub + i + 1]);
+                    uint64_t& sum = l[(b * kSub + i) / 2];
+                    const uint64_t w2 = ptx::f2_pack(w[i], w[i + 1]);
+                    sum = kE ? ptx::f2_fma(w2, inv2, sum) : ptx::f2_add(w2, sum);
                 }
-                store_weights<kE, kR>(w, p_row, r & 7, c0 + b * kSub, keep);
+                if (kE && zero) {
+#pragma unroll
+                    for (int i = 0; i < kSub; ++i) w[i] = 0.f;
+                }
+                store_weights<kE, kR>(w, p_row, r & 7, c0 + b * kSub);
             }
             if (key0 + 127 >= it.r.end) {
                 // Slots past the end hold anything: zero them before 0 * NaN.
+                // V's tile in the ring: K0, then K(j+1), V(j) in turn.
+                const uint32_t v_used = used + (j + 1 < it.m ? 2 * j + 2 : 2 * it.m - 1);
                 wait(&tl.full[v_used % S::kSlots], (v_used / S::kSlots) & 1);
                 if (key >= it.r.end && group == 0) {
                     uint4* row = reinterpret_cast<uint4*>(ring + (v_used % S::kSlots) * S::kTile +
@@ -854,11 +907,22 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
         }
         used += 2 * it.m;
 
+        // The next item's queries: its scores run during this one's epilogue.
+        Cursor next = c;
+        cursor_next(p, next, it);
+        Item next_it = it;
+        ++items;
+        if (next.left > 0) {
+            next_it = cursor_item(p, next);
+            stage(next_it, next.h);
+        }
+
         // The item's result, or the share's part of it.
-        const float mine = lane_sums<kCols>(l, lane);
+        float sums[kCols];
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) ptx::f2_unpack(l[i], sums[2 * i], sums[2 * i + 1]);
+        const float mine = lane_sums<kCols>(sums, lane);
         if (lane < kCols) tl.wmax[quarter][c0 + lane] = mine;
-        wait(&tl.pv_done, (g - 1) & 1);
-        ptx::tc_fence_after();
         group_sync(bar_id);
         const bool whole = c.j == 0 && it.m == it.r.n;
         const long long slot = static_cast<long long>(blockIdx.x) * 2 + (c.j == 0 ? 1 : 0);
@@ -866,32 +930,41 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
             const int col = c0 + r;
             const float sum = (tl.wmax[0][col] + tl.wmax[1][col]) +
                               (tl.wmax[2][col] + tl.wmax[3][col]);
-            const int row = tl.row[col];
+            const int row = rows.row[col];
             if (whole) {
                 if (row >= 0) {
                     const int q = row / p.h_q;
                     p.lse[static_cast<long long>(row - q * p.h_q) * p.total_q + q] =
-                        sum > 0.f ? (log2f(sum) - tl.neg_m[col]) * 0.69314718055994531f
+                        sum > 0.f ? (log2f(sum) - rows.offset[col]) * 0.69314718055994531f
                                   : -CUDART_INF_F;
                 }
-                tl.limit[col] = sum > 0.f ? 1.f / sum : 0.f;
+                tl.alpha[col] = sum > 0.f ? 1.f / sum : 0.f;
             } else {
-                p.part_ml[slot * kR + col] = make_float2(-tl.neg_m[col], sum);
+                p.part_ml[slot * kR + col] = make_float2(-rows.offset[col], sum);
             }
         }
+        wait(&tl.pv_done, (g - 1) & 1);
+        ptx::tc_fence_after();
         group_sync(bar_id);
 #pragma unroll
-        for (int b = 0; b < kCols / kSub; ++b) {
-            float o[kSub];
-            tmem_load(o_tm + b * kSub, o);
+        for (int b = 0; b < kCols / 8; ++b) {
+            float o[8];
+            tmem_load(o_tm + b * 8, o);
+            if constexpr (S::kSideBySide) {
+                float o1[8], o2[8];
+                tmem_load(o_tm + S::kN + b * 8, o1);
+                tmem_load(o_tm + 2 * S::kN + b * 8, o2);
 #pragma unroll
-            for (int i = 0; i < kSub; ++i) {
-                const int col = c0 + b * kSub + i;
+                for (int i = 0; i < 8; ++i) o[i] += o1[i] + o2[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int col = c0 + b * 8 + i;
                 if (whole) {
-                    const int row = tl.row[col];
+                    const int row = rows.row[col];
                     if (row >= 0)
                         p.o[static_cast<long long>(row) * kHeadDim + r] =
-                            __float2bfloat16_rn(o[i] * tl.limit[col]);
+                            __float2bfloat16_rn(o[i] * tl.alpha[col]);
                 } else {
                     p.part_o[(slot * kR + col) * kHeadDim + r] = o[i];
                 }
@@ -902,7 +975,7 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
             // It begins here and goes on in the next shares.
             tail_part = true;
             if (threadIdx.x == 0) {
-                const int head0 = (c.h % p.head_tiles) * p.heads_per_tile;
+                const int head0 = (c.h - head * p.head_tiles) * p.heads_per_tile;
                 const long long last = tl.begin + tl.chunk - it.m + it.r.n - 1;
                 p.meta[blockIdx.x] =
                     make_int4(static_cast<int>(last / tl.chunk - blockIdx.x) + 1,
@@ -911,8 +984,9 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
                                   (min(p.heads_per_tile, p.group - head0) << 16));
             }
         }
-        group_sync(bar_id);  // the rows' arrays are free for the next item
-        cursor_next(p, c, it);
+        group_sync(bar_id);  // wmax and alpha are free
+        c = next;
+        it = next_it;
     }
     if (threadIdx.x == 0 && !tail_part) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
 }
@@ -981,11 +1055,67 @@ __global__ void __launch_bounds__(Shape<kE, kR>::kThreads, Shape<kE, kR>::kCtasP
 }
 
 // ------------------------------------------------------------------ merge
-// The parts of the items that a share's border cuts.  Block (c, y): the item
-// that begins in share c and goes on, rows y, y + 8, ...; a warp takes every
-// eighth part, and the warps' sums are joined in order.
+// The parts of the items that a share's border cuts:
 //     O = sum_i 2^(u_i - U) acc_i / sum_i 2^(u_i - U) l_i,   U = max u_i.
+// Blocks (c, y): the item that begins in share c and goes on in the next ones.
+// With at most kMergeWarps parts a warp takes a row, rows 8 y .. 8 y + 7 to a
+// block; with more (long keys, few rows) a block takes rows y, y + 8, ... and a
+// warp every eighth part, and the warps' sums are joined in order.
 constexpr int kMergeWarps = 8;
+constexpr int kMergeParts = 8;  // parts whose loads are in flight together
+
+struct Merged {
+    float u, l;
+    float4 acc;
+};
+
+// The sum of parts first, first + step, ... (fewer than `parts`) of a row.
+__device__ __forceinline__ Merged merge_parts(const float2* ml, const float4* o, int first,
+                                              int step, int parts, long long stride, int lane) {
+    Merged r;
+    r.u = -CUDART_INF_F;
+    r.l = 0.f;
+    r.acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = first; i0 < parts; i0 += kMergeParts * step) {
+        float2 m[kMergeParts];
+        float4 x[kMergeParts];
+#pragma unroll
+        for (int k = 0; k < kMergeParts; ++k) {
+            const int i = i0 + k * step;
+            // Part 0 is the second of its share, the others the first of theirs.
+            const long long at = i < parts ? (2LL * i + (i == 0 ? 1 : 0)) * stride : stride;
+            m[k] = ml[at];
+            x[k] = o[at * 32 + lane];
+        }
+        float u = r.u;
+#pragma unroll
+        for (int k = 0; k < kMergeParts; ++k) {
+            if (i0 + k * step >= parts || !(m[k].y > 0.f)) m[k] = make_float2(-CUDART_INF_F, 0.f);
+            u = fmaxf(u, m[k].x);
+        }
+        const float ref = u > -CUDART_INF_F ? u : 0.f;
+        const float keep = exp2f(r.u - ref);
+        r.l *= keep;
+        r.acc.x *= keep;
+        r.acc.y *= keep;
+        r.acc.z *= keep;
+        r.acc.w *= keep;
+#pragma unroll
+        for (int k = 0; k < kMergeParts; ++k) {
+            const float a = exp2f(m[k].x - ref);
+            if (a > 0.f) {
+                r.l = fmaf(a, m[k].y, r.l);
+                r.acc.x = fmaf(a, x[k].x, r.acc.x);
+                r.acc.y = fmaf(a, x[k].y, r.acc.y);
+                r.acc.z = fmaf(a, x[k].z, r.acc.z);
+                r.acc.w = fmaf(a, x[k].w, r.acc.w);
+            }
+        }
+        r.u = u;
+    }
+    return r;
+}
+
 template <int kR>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     attn_cache_merge_kernel(const __grid_constant__ FwdCacheParams p) {
@@ -995,57 +1125,57 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     if (parts <= 0) return;
     const int queries = meta.w & 0xffff, heads = meta.w >> 16;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto write = [&](int c, const Merged& m) {
+        const int qi = p.div_heads.div(c), e = c - qi * p.heads_per_tile;
+        const float inv = m.l > 0.f ? 1.f / m.l : 0.f;
+        const int q = meta.y + qi, h = meta.z + e;
+        reinterpret_cast<uint2*>(p.o + (static_cast<long long>(q) * p.h_q + h) * kHeadDim)[lane] =
+            make_uint2(ptx::pack_bf16x2(m.acc.x * inv, m.acc.y * inv),
+                       ptx::pack_bf16x2(m.acc.z * inv, m.acc.w * inv));
+        if (lane == 0)
+            p.lse[static_cast<long long>(h) * p.total_q + q] =
+                m.l > 0.f ? (log2f(m.l) + m.u) * 0.69314718055994531f : -CUDART_INF_F;
+    };
+    auto there = [&](int c) -> bool {
+        const int qi = p.div_heads.div(c), e = c - qi * p.heads_per_tile;
+        return c < kR && qi < queries && e < heads;
+    };
+    const long long share = static_cast<long long>(blockIdx.x) * 2 * kR;
+    const float2* ml = p.part_ml + share;
+    const float4* o = reinterpret_cast<const float4*>(p.part_o) + share * 32;
+    if (parts <= kMergeWarps) {
+        const int c = blockIdx.y * kMergeWarps + warp;
+        if (there(c)) write(c, merge_parts(ml + c, o + c * 32, 0, 1, parts, kR, lane));
+        return;
+    }
     __shared__ float4 acc_s[kMergeWarps][32];
     __shared__ float2 ml_s[kMergeWarps];
     for (int c = blockIdx.y; c < kR; c += gridDim.y) {
-        const int qi = c / p.heads_per_tile, e = c - qi * p.heads_per_tile;
-        if (qi >= queries || e >= heads) continue;  // the same for the whole block
-        auto slot = [&](int i) -> long long {
-            return (static_cast<long long>(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * kR + c;
-        };
-        float u = -CUDART_INF_F;
-        for (int i = lane; i < parts; i += 32) {
-            const float2 ml = p.part_ml[slot(i)];
-            if (ml.y > 0.f) u = fmaxf(u, ml.x);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, o));
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f;
-        if (u > -CUDART_INF_F) {
-#pragma unroll 4
-            for (int i = warp; i < parts; i += kMergeWarps) {
-                const float2 ml = p.part_ml[slot(i)];
-                const float4 x =
-                    reinterpret_cast<const float4*>(p.part_o + slot(i) * kHeadDim)[lane];
-                const float a = ml.y > 0.f ? exp2f(ml.x - u) : 0.f;
-                l = fmaf(a, ml.y, l);
-                acc.x = fmaf(a, x.x, acc.x);
-                acc.y = fmaf(a, x.y, acc.y);
-                acc.z = fmaf(a, x.z, acc.z);
-                acc.w = fmaf(a, x.w, acc.w);
-            }
-        }
-        acc_s[warp][lane] = acc;
-        if (lane == 0) ml_s[warp].y = l;
+        if (!there(c)) continue;  // the same for the whole block
+        const Merged m = merge_parts(ml + c, o + c * 32, warp, kMergeWarps, parts, kR, lane);
+        acc_s[warp][lane] = m.acc;
+        if (lane == 0) ml_s[warp] = make_float2(m.u, m.l);
         __syncthreads();
         if (warp == 0) {
-            for (int w = 1; w < kMergeWarps; ++w) {
-                const float4 x = acc_s[w][lane];
-                acc.x += x.x;
-                acc.y += x.y;
-                acc.z += x.z;
-                acc.w += x.w;
-                l += ml_s[w].y;
+            Merged t;
+            t.u = -CUDART_INF_F;
+            t.l = 0.f;
+            t.acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kMergeWarps; ++w) t.u = fmaxf(t.u, ml_s[w].x);
+            if (t.u > -CUDART_INF_F) {
+#pragma unroll
+                for (int w = 0; w < kMergeWarps; ++w) {
+                    const float a = exp2f(ml_s[w].x - t.u);
+                    const float4 x = acc_s[w][lane];
+                    t.l = fmaf(a, ml_s[w].y, t.l);
+                    t.acc.x = fmaf(a, x.x, t.acc.x);
+                    t.acc.y = fmaf(a, x.y, t.acc.y);
+                    t.acc.z = fmaf(a, x.z, t.acc.z);
+                    t.acc.w = fmaf(a, x.w, t.acc.w);
+                }
             }
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-            const int q = meta.y + qi, h = meta.z + e;
-            reinterpret_cast<uint2*>(p.o + (static_cast<long long>(q) * p.h_q + h) * kHeadDim)[lane] =
-                make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv),
-                           ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
-            if (lane == 0)
-                p.lse[static_cast<long long>(h) * p.total_q + q] =
-                    l > 0.f ? (log2f(l) + u) * 0.69314718055994531f : -CUDART_INF_F;
+            write(c, t);
         }
         __syncthreads();
     }
