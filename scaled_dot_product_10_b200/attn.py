@@ -7,6 +7,7 @@ fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -23,6 +24,7 @@ STATIC_STAGING_BYTES = 32 << 20
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libattn_sm100.so"
 _lib = None
+_CURRENT = contextlib.nullcontext()
 
 # (name, restype, argtypes) of every exported entry point.
 _P = ctypes.c_void_p
@@ -100,8 +102,10 @@ def attn_strerror(code: int) -> str:
 
 def _stream_handle(stream) -> int | None:
     if stream is None:
+        # torch.cuda.current_stream().cuda_stream without the stream object
+        # (which took 4 us of a call's 20).
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -140,6 +144,8 @@ def _on_device(dev):
     """Context making ``dev`` the current device for the library call (and
     for the default stream, torch's current stream on that device)."""
     import torch
+    if dev.index == torch.cuda.current_device():
+        return _CURRENT
     return torch.cuda.device(dev)
 
 
@@ -525,32 +531,44 @@ class KVCache:
         self._ref = ctypes.addressof(self._struct)
 
 
-def _packed_rows(name, t, heads=None):
-    """Checks a [tokens, heads, 128] BF16 tensor whose heads are contiguous
-    within a token; returns its token stride."""
-    import torch
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be bfloat16")
-    if t.dim() != 3 or t.shape[2] != 128 or (heads is not None and t.shape[1] != heads):
+def _packed_rows(name, t, heads, dtype):
+    """Checks a [tokens, heads, 128] tensor whose heads are contiguous within
+    a token; returns its token stride."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != 128 or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} must be [tokens, {'heads' if heads is None else heads}, 128]")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != 128):
+    token, head, one = t.stride()
+    if one != 1 or (head != 128 and shape[1] > 1):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * 128
+    return token if shape[0] > 1 else shape[1] * 128
 
 
-def _cache_batch(cache, page_table, seqlens_k, cu, cu_name):
+def _cache_batch(page_table, seqlens_k, cu, cu_name, int32):
     """Checks a step's int32 tensors; returns (batch, max_pages)."""
-    import torch
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_contiguous():
+    shape = page_table.shape
+    if page_table.dtype != int32 or len(shape) != 2 or not page_table.is_contiguous():
         raise ValueError("page_table must be a contiguous int32 [batch, max_pages]")
-    batch, max_pages = page_table.shape
-    if seqlens_k.dtype != torch.int32 or tuple(seqlens_k.shape) != (batch,) \
-            or not seqlens_k.is_contiguous():
+    if seqlens_k.dtype != int32 or seqlens_k.shape != shape[:1] or not seqlens_k.is_contiguous():
         raise ValueError("seqlens_k must be a contiguous int32 [batch]")
-    if cu is not None and (cu.dtype != torch.int32 or tuple(cu.shape) != (batch + 1,)
+    if cu is not None and (cu.dtype != int32 or cu.dim() != 1 or cu.shape[0] != shape[0] + 1
                            or not cu.is_contiguous()):
         raise ValueError(f"{cu_name} must be a contiguous int32 [batch + 1]")
-    return batch, max_pages
+    return shape
+
+
+def _same_device(cache, stream, tensors):
+    """The cache's device, which every tensor of a call (and a torch stream)
+    must share."""
+    dev = cache.device
+    for name, t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
+    sdev = getattr(stream, "device", None)
+    if sdev is not None and sdev != dev:
+        raise ValueError(f"stream belongs to {sdev}, the cache to {dev}")
+    return dev
 
 
 def attn_cache_append(cache: KVCache, k, v, page_table, seqlens_k, cu_seqlens=None,
@@ -572,40 +590,41 @@ def attn_cache_append(cache: KVCache, k, v, page_table, seqlens_k, cu_seqlens=No
     One launch; rows behind the last sequence are neither read nor written.
     """
     import torch
-    total, h_kv = k.shape[0], cache.h_kv
-    k_stride = _packed_rows("k", k, h_kv)
-    v_stride = _packed_rows("v", v, h_kv)
+    bf16, h_kv = torch.bfloat16, cache.h_kv
+    k_stride = _packed_rows("k", k, h_kv, bf16)
+    v_stride = _packed_rows("v", v, h_kv, bf16)
+    total = k.shape[0]
     if v.shape[0] != total:
         raise ValueError("k, v shapes disagree")
-    batch, max_pages = _cache_batch(cache, page_table, seqlens_k, cu_seqlens, "cu_seqlens")
-    tensors = dict(k=k, v=v, page_table=page_table, seqlens_k=seqlens_k)
-    h_q, q_stride, rotary_dim = h_kv, 0, 0
+    batch, max_pages = _cache_batch(page_table, seqlens_k, cu_seqlens, "cu_seqlens", torch.int32)
+    h_q = h_kv
+    q_stride = rotary_dim = 0
+    q_ptr = q_out_ptr = cu_ptr = freq_ptr = None
     if q is not None:
-        q_stride, h_q = _packed_rows("q", q), q.shape[1]
+        q_stride = _packed_rows("q", q, None, bf16)
+        h_q = q.shape[1]
         if q.shape[0] != total:
             raise ValueError("q, k shapes disagree")
-        tensors["q"] = q
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    if cu_seqlens is not None:
-        tensors["cu_seqlens"] = cu_seqlens
     if inv_freq is not None:
         if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be a contiguous float32 vector")
-        tensors["inv_freq"], rotary_dim = inv_freq, 2 * inv_freq.numel()
-    dev = _cuda_device(stream, **tensors)
-    if dev != cache.device:
-        raise ValueError(f"the cache is on {cache.device}, the call's tensors on {dev}")
-    if total == 0:
-        return None if q is None else _out(q, q_out, "q_out", q.shape, torch.bfloat16, stream)
+        rotary_dim, freq_ptr = 2 * inv_freq.shape[0], inv_freq.data_ptr()
+    dev = _same_device(cache, stream, (("k", k), ("v", v), ("page_table", page_table),
+                                       ("seqlens_k", seqlens_k), ("cu_seqlens", cu_seqlens),
+                                       ("q", q), ("inv_freq", inv_freq)))
     with _on_device(dev):
         if q is not None:
-            q_out = _out(q, q_out, "q_out", (total, h_q, 128), torch.bfloat16, stream)
+            q_out = _out(q, q_out, "q_out", (total, h_q, 128), bf16, stream)
+            q_ptr, q_out_ptr = q.data_ptr(), q_out.data_ptr()
+        if cu_seqlens is not None:
+            cu_ptr = cu_seqlens.data_ptr()
+        if total == 0:
+            return q_out
         rc = load_library().attn_cache_append(
-            cache._ref, k.data_ptr(), v.data_ptr(), None if q is None else q.data_ptr(),
-            None if q is None else q_out.data_ptr(), page_table.data_ptr(), seqlens_k.data_ptr(),
-            None if cu_seqlens is None else cu_seqlens.data_ptr(),
-            None if inv_freq is None else inv_freq.data_ptr(), batch, max_pages, total,
+            cache._ref, k.data_ptr(), v.data_ptr(), q_ptr, q_out_ptr, page_table.data_ptr(),
+            seqlens_k.data_ptr(), cu_ptr, freq_ptr, batch, max_pages, total,
             int(total if max_seqlen is None else max_seqlen), h_q, k_stride, v_stride, q_stride,
             rotary_dim, int(bool(interleaved)), _stream_handle(stream))
     if rc != ATTN_OK:
@@ -633,15 +652,12 @@ def attn_fwd_cache(q, cache: KVCache, page_table, seqlens_k, cu_seqlens_q=None,
     :func:`cache_workspace_bytes` bytes, allocated here if None.  Two launches.
     """
     import torch
-    q_stride = _packed_rows("q", q)
+    q_stride = _packed_rows("q", q, None, torch.bfloat16)
     total_q, h_q, d = q.shape
-    batch, max_pages = _cache_batch(cache, page_table, seqlens_k, cu_seqlens_q, "cu_seqlens_q")
-    tensors = dict(q=q, page_table=page_table, seqlens_k=seqlens_k)
-    if cu_seqlens_q is not None:
-        tensors["cu_seqlens_q"] = cu_seqlens_q
-    dev = _cuda_device(stream, **tensors)
-    if dev != cache.device:
-        raise ValueError(f"the cache is on {cache.device}, the call's tensors on {dev}")
+    batch, max_pages = _cache_batch(page_table, seqlens_k, cu_seqlens_q, "cu_seqlens_q",
+                                    torch.int32)
+    dev = _same_device(cache, stream, (("q", q), ("page_table", page_table),
+                                       ("seqlens_k", seqlens_k), ("cu_seqlens_q", cu_seqlens_q)))
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if max_seqlen_q is None:
@@ -650,11 +666,10 @@ def attn_fwd_cache(q, cache: KVCache, page_table, seqlens_k, cu_seqlens_q=None,
         o, lse = _outputs(q, o, lse, (total_q, h_q, d), (h_q, total_q), stream)
         if total_q == 0:
             return o, lse
+        nbytes = 0
         if workspace is None:
-            workspace = _workspace(q, None, cache_workspace_bytes(h_q, cache.h_kv, max_seqlen_q),
-                                   stream)
-        else:
-            workspace = _workspace(q, workspace, 0, stream)
+            nbytes = cache_workspace_bytes(h_q, cache.h_kv, max_seqlen_q)
+        workspace = _workspace(q, workspace, nbytes, stream)
         rc = load_library().attn_fwd_cache(
             cache._ref, q.data_ptr(), o.data_ptr(), lse.data_ptr(), page_table.data_ptr(),
             seqlens_k.data_ptr(), None if cu_seqlens_q is None else cu_seqlens_q.data_ptr(),
