@@ -101,6 +101,7 @@ int cache_rows(int group, int max_seqlen) {
     return rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : 64));
 }
 
+constexpr int kWholeTiles = 4;      // see attn_fwd_cache
 constexpr int kCacheCtasPerSm = 2;  // of any variant, at most
 
 struct CacheWorkspace {
@@ -143,6 +144,8 @@ int launch_fwd_cache(const CUtensorMap& tk, const CUtensorMap& tv, const cache::
     if (launch_after(cache::attn_fwd_cache_kernel<kE, kR>, dim3(grid), S::kThreads, S::kAlloc, cs,
                      tk, tv, p) != cudaSuccess)
         return ATTN_ERR_CUDA;
+    g_last_launches = 1;
+    if (p.whole) return ATTN_OK;
     if (launch_after(cache::attn_cache_merge_kernel<kR>, dim3(grid, 8), cache::kMergeWarps * 32, 0,
                      cs, p) != cudaSuccess)
         return ATTN_ERR_CUDA;
@@ -282,6 +285,8 @@ extern "C" int attn_fwd_cache(const attn_cache_t* c, const void* q, void* o, flo
     p.heads_per_tile = std::min(p.group, rows);
     p.q_per_tile = rows / p.heads_per_tile;
     p.head_tiles = (p.group + p.heads_per_tile - 1) / p.heads_per_tile;
+    // Table rows of at most kWholeTiles key tiles: an item is one CTA's, and no
+    // merge is launched.
     // The share of a CTA has 32-bit numbers of units (row tiles x key tiles).
     const long long cap = static_cast<long long>(max_pages) * c->page_size;
     const long long key_tiles = std::min(cap, kMaxInt) / 128 + 1;
@@ -293,6 +298,7 @@ extern "C" int attn_fwd_cache(const attn_cache_t* c, const void* q, void* o, flo
                             ((p.max_seqlen_q + p.q_per_tile - 1) / p.q_per_tile)) *
         c->h_kv * p.head_tiles;
     if (row_tiles > kMaxInt || row_tiles * key_tiles / 64 > kMaxInt) return ATTN_ERR_INVALID;
+    p.whole = cap <= 128 * kWholeTiles;
 
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;
@@ -329,7 +335,7 @@ extern "C" int attn_fwd_cache(const attn_cache_t* c, const void* q, void* o, flo
     p.part_o = reinterpret_cast<float*>(ws + w.o);
     p.timeout_ns = g_timeout_ns;
     p.status = st->status;
-    const long long most = row_tiles * key_tiles;
+    const long long most = p.whole ? row_tiles : row_tiles * key_tiles;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const int sms = st->num_sms;
     if (c->type == ATTN_CACHE_E4M3) {

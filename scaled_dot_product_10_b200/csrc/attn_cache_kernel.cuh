@@ -65,6 +65,7 @@ struct FwdCacheParams {
     int q_per_tile;      // queries of a row tile
     int head_tiles;      // row tiles across the group's heads
     int causal, window;  // window -1: none
+    int whole;           // shares are of whole items: nothing to merge
     float scale_log2;    // scale * log2(e)
     float* part_o;       // [ctas][2][R][128]
     float2* part_ml;     // [ctas][2][R]: log2 of the unit of weights, row sum in it
@@ -114,7 +115,13 @@ __device__ __forceinline__ RowTile row_tile(const FwdCacheParams& p, const Seq& 
     return r;
 }
 
+// Units of work of a row tile, of which a share has a run.
+__device__ __forceinline__ int tile_units(const FwdCacheParams& p, const Seq& s, int t) {
+    return p.whole ? 1 : row_tile(p, s, t).n;
+}
+
 __device__ __forceinline__ long long seq_units(const FwdCacheParams& p, const Seq& s) {
+    if (p.whole) return s.tiles;
     long long u = 0;
     for (int t = 0; t < s.tiles; ++t) u += row_tile(p, s, t).n;
     return u;
@@ -136,12 +143,12 @@ __device__ __forceinline__ Item cursor_item(const FwdCacheParams& p, const Curso
     Item it;
     it.s = load_seq(p, c.b);
     it.r = row_tile(p, it.s, c.t);
-    it.m = min(it.r.n - c.j, c.left);
+    it.m = p.whole ? it.r.n : min(it.r.n - c.j, c.left);
     return it;
 }
 
 __device__ __forceinline__ void cursor_next(const FwdCacheParams& p, Cursor& c, const Item& it) {
-    c.left -= it.m;
+    c.left -= p.whole ? 1 : it.m;
     c.j = 0;
     if (++c.t < it.s.tiles) return;
     c.t = 0;
@@ -276,7 +283,7 @@ struct Shape {
     static constexpr int kOffQ = 0;
     static constexpr int kOffP = kOffQ + (kQPieces * kQPiece + 1023) / 1024 * 1024;
     static constexpr int kOffRing = kOffP + kPBytes;
-    static constexpr int kTail = 4608;  // barriers and the small arrays below
+    static constexpr int kTail = 5632;  // barriers and the small arrays below
     // Two CTAs of an SM overlap one's softmax with the other's products.  Ring
     // and P of BF16 pages leave room for one, whose deeper ring has the same
     // bytes in flight.
@@ -284,6 +291,9 @@ struct Shape {
     static constexpr int kBudget = (kE ? 113 : 227) * 1024 - 1024;
     static constexpr int kSlots = (kBudget - kOffRing - kTail) / kTile;
     static_assert(kSlots >= 3 && kSlots <= 8, "the ring needs K(j+1) beside K(j) and V(j)");
+    // The scales of tile g + 4 are written over those of tile g once a slot is
+    // free for K(g+4); then V(g), kSlots tiles before it, has been used.
+    static_assert(!kE || kSlots <= 5, "four tiles' scales are kept");
     static constexpr int kOffTail = kOffRing + kSlots * kTile;
     static constexpr int kAlloc = kOffTail + kTail + 1024;
     // The pieces of P side by side are one product of 3 kN columns, of which
@@ -312,6 +322,9 @@ struct Tail {
     Rows rows[2];  // of this item and the next
     float wmax[4][kMaxRows];
     float alpha[kMaxRows];
+    // Scales of the last tiles' boxes (E4M3): K's, log2 of V's, 1 / V's, V's is 0.
+    float4 scales[4][16];
+    uint64_t scales_full[4];
     uint64_t full[8], empty[8];
     uint64_t q_full, s_full[2], s_free[2], p_full, pv_done, drain;
     long long begin;  // first unit of this share
@@ -321,7 +334,7 @@ struct Tail {
     Cursor cursor;
     int chunk;  // units of every share
 };
-static_assert(sizeof(Tail) <= 4608, "");
+static_assert(sizeof(Tail) <= 5632, "");
 
 // Where this CTA's share of the units begins (every thread of the CTA calls).
 template <int kThreads>
@@ -383,7 +396,7 @@ __device__ __forceinline__ void find_share(const FwdCacheParams& p, Tail& tl) {
                     left = static_cast<int>(rem) % static_cast<int>(own);
                 }
                 for (;; ++t) {
-                    const int n = row_tile(p, s, t).n;
+                    const int n = tile_units(p, s, t);
                     if (left < n) break;
                     left -= n;
                 }
@@ -398,7 +411,8 @@ __device__ __forceinline__ void find_share(const FwdCacheParams& p, Tail& tl) {
 }
 
 // ------------------------------------------------------------------ producer
-// One warp: lane i loads the tile's i-th box of page_size-dividing keys.
+// One warp: lane i loads the tile's i-th box (a run of keys of one page), and
+// with E4M3 pages keeps the box's scales one tile ahead and its page two.
 template <bool kE, int kR>
 __device__ __forceinline__ void producer_role(const FwdCacheParams& p, const CUtensorMap* tm_k,
                                               const CUtensorMap* tm_v, Tail& tl, uint32_t ring,
@@ -406,28 +420,40 @@ __device__ __forceinline__ void producer_role(const FwdCacheParams& p, const CUt
     using S = Shape<kE, kR>;
     const int boxes = 128 / p.box;
     const uint32_t box_bytes = static_cast<uint32_t>(p.box) * 128u;  // of one 128-byte column
-    uint32_t loads = 0;
+    uint32_t loads = 0, g = 0;
     bool ok = true;
     Cursor c = tl.cursor;
     while (ok && c.left > 0) {
         const Item it = cursor_item(p, c);
         const int head = c.h / p.head_tiles;
         const int* table = p.table + static_cast<long long>(c.b) * p.max_pages;
-        auto page_of = [&](int tile) -> int {  // this lane's page; -1 past the last key
-            const int key = (it.r.tile0 + c.j + tile) * 128 + lane * p.box;
-            return lane < boxes && key < it.r.end ? table[p.div_page.div(key)] : -1;
+        const int key_of_lane = (it.r.tile0 + c.j) * 128 + lane * p.box;
+        // This lane's box holds keys of the item.
+        auto mine = [&](int tile) -> bool {
+            return tile < it.m && lane < boxes && key_of_lane + tile * 128 < it.r.end;
+        };
+        auto page_of = [&](int tile) -> int {
+            return mine(tile) ? table[p.div_page.div(key_of_lane + tile * 128)] : -1;
+        };
+        auto scales_of = [&](int page, float& ks, float& vs) {
+            ks = vs = 0.f;
+            if (page >= 0 && page < p.num_pages) {
+                const long long at = static_cast<long long>(page) * p.h_kv + head;
+                ks = p.k_scale[at];
+                vs = p.v_scale[at];
+            }
         };
         auto load = [&](const CUtensorMap* tm, int tile, int page) -> bool {
             const int slot = loads % S::kSlots;
             if (!wait_bar_warp(ptx::smem_u32(&tl.empty[slot]), ((loads / S::kSlots) & 1) ^ 1, wc))
                 return false;
-            const int key = (it.r.tile0 + c.j + tile) * 128 + lane * p.box;
-            const bool mine = lane < boxes && key < it.r.end;
-            const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));
+            const bool m = mine(tile);
+            const uint32_t n = __popc(__ballot_sync(0xffffffffu, m));
             const uint32_t bar = ptx::smem_u32(&tl.full[slot]);
             if (lane == 0) ptx::mbar_arrive_expect_tx(bar, n * box_bytes * S::kElem);
             __syncwarp();
-            if (mine) {
+            if (m) {
+                const int key = key_of_lane + tile * 128;
                 const uint32_t dst = ring + slot * S::kTile + lane * box_bytes;
                 const int at = key - p.div_page.div(key) * p.page_size;
                 tma_load_page(dst, tm, bar, 0, head, at, page);
@@ -436,14 +462,31 @@ __device__ __forceinline__ void producer_role(const FwdCacheParams& p, const CUt
             ++loads;
             return true;
         };
-        int page = page_of(0);
-        ok = load(tm_k, 0, page);
-        for (int i = 0; i < it.m && ok; ++i) {
-            int next = 0;
-            if (i + 1 < it.m) {
-                next = page_of(i + 1);
-                ok = load(tm_k, i + 1, next);
+        float ks = 0.f, vs = 0.f;  // of the tile whose K comes next
+        int page = page_of(0);     // of the tile whose V comes next
+        int ahead = page_of(1);    // of the tile after it
+        if constexpr (kE) scales_of(page, ks, vs);
+        // K of a tile, then its scales.
+        auto load_k = [&](int tile, int pg) -> bool {
+            if (!load(tm_k, tile, pg)) return false;
+            if constexpr (kE) {
+                if (lane < 16) {
+                    const float lv = fminf(fmaxf(__log2f(vs), -64.f), 64.f);
+                    tl.scales[g & 3][lane] =
+                        make_float4(ks, lv, ptx::ex2(-lv), vs >= 0x1p-64f ? 0.f : 1.f);
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&tl.scales_full[g & 3]));
+                ++g;
             }
+            return true;
+        };
+        ok = load_k(0, page);
+        for (int i = 0; i < it.m && ok; ++i) {
+            const int next = ahead;
+            if constexpr (kE) scales_of(next, ks, vs);
+            ahead = page_of(i + 2);
+            if (i + 1 < it.m) ok = load_k(i + 1, next);
             if (ok) ok = load(tm_v, i, page);
             page = next;
         }
@@ -710,6 +753,7 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_tm = tmem + lanes + c0, o_tm = tmem + lanes + 2 * S::kN + c0;
     const uint32_t p_row = sp + r * 128;
+    const int box_log2 = 31 - __clz(p.box);
     uint32_t g = 0, used = 0, items = 0;
     bool dead = false;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -732,62 +776,36 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
     while (c.left > 0) {
         Rows& rows = tl.rows[items & 1];
         const int head = c.h / p.head_tiles;
-        const int* table = p.table + static_cast<long long>(c.b) * p.max_pages;
         const int shift = it.s.len - it.s.n;
         const int min_last = p.causal ? min(it.s.kv - 1, shift + it.r.i0) : it.s.kv - 1;
         const int max_first = p.window >= 0 ? shift + it.r.i1 - p.window : 0;
-        // Scales of this thread's key: the page one tile ahead, its scales in flight.
-        auto page_of = [&](int tile) -> int {
-            const int key = (it.r.tile0 + c.j + tile) * 128 + r;
-            return key < it.r.end ? table[p.div_page.div(key)] : -1;
-        };
-        float ks_next = 0.f, vs_next = 0.f;
-        int page_next = -1;
-        auto scales_of = [&](int page, float& a, float& b) {
-            a = b = 0.f;
-            if (page >= 0 && page < p.num_pages) {
-                const long long at = static_cast<long long>(page) * p.h_kv + head;
-                a = p.k_scale[at];
-                b = p.v_scale[at];
-            }
-        };
-        if constexpr (kE) {
-            const int page = page_of(0);
-            page_next = it.m > 1 ? page_of(1) : -1;
-            scales_of(page, ks_next, vs_next);
-        }
         uint64_t l[kPairs];
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) l[i] = 0;
 
         for (int j = 0; j < it.m; ++j, ++g) {
             // Scores become exponents: x = S scale ks + log2(vs) + offset.
-            float ks = p.scale_log2, lv = 0.f, inv_vs = 1.f;
-            bool zero = false;
+            float4 sc = make_float4(p.scale_log2, 0.f, 1.f, 0.f);
             if constexpr (kE) {
-                ks = ks_next;
-                const float vs = vs_next;
-                scales_of(page_next, ks_next, vs_next);
-                page_next = j + 2 < it.m ? page_of(j + 2) : -1;
-                lv = fminf(fmaxf(__log2f(vs), -64.f), 64.f);
-                inv_vs = ptx::ex2(-lv);
-                zero = !(vs >= 0x1p-64f);  // V is taken as zero; its weight stays in l
+                wait(&tl.scales_full[g & 3], (g >> 2) & 1);
+                sc = tl.scales[g & 3][r >> box_log2];
             }
-            const uint64_t ks2 = ptx::f2_pack(ks, ks), lv2 = ptx::f2_pack(lv, lv);
+            const uint64_t ks2 = ptx::f2_pack(sc.x, sc.x), lv2 = ptx::f2_pack(sc.y, sc.y);
             const int key0 = (it.r.tile0 + c.j + j) * 128, key = key0 + r;
             const bool masked = key0 + 127 > min_last || key0 < max_first;
             const uint32_t s_at = s_tm + (g & 1) * S::kN;
-            float x[kCols];
-            auto exponents = [&](bool absolute) {
-                tmem_load(s_at, x);
+            // Of kSub columns; `absolute`: without the offset.
+            auto exponents = [&](float (&x)[kSub], int b, bool absolute) {
+                tmem_load(s_at + b * kSub, x);
+                const int cb = c0 + b * kSub;
 #pragma unroll
-                for (int i = 0; i < kCols; i += 4) {
+                for (int i = 0; i < kSub; i += 4) {
                     const float4 o = absolute ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                              : *reinterpret_cast<const float4*>(&rows.offset[c0 + i]);
+                                              : *reinterpret_cast<const float4*>(&rows.offset[cb + i]);
                     uint64_t o2[2] = {ptx::f2_pack(o.x, o.y), ptx::f2_pack(o.z, o.w)};
                     uint64_t x2[2] = {ptx::f2_pack(x[i], x[i + 1]), ptx::f2_pack(x[i + 2], x[i + 3])};
                     if constexpr (kE) {
-                        const float4 q = *reinterpret_cast<const float4*>(&rows.scale[c0 + i]);
+                        const float4 q = *reinterpret_cast<const float4*>(&rows.scale[cb + i]);
                         x2[0] = ptx::f2_mul(x2[0], ptx::f2_pack(q.x, q.y));
                         x2[1] = ptx::f2_mul(x2[1], ptx::f2_pack(q.z, q.w));
                         o2[0] = ptx::f2_add(o2[0], lv2);
@@ -798,27 +816,36 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
                 }
                 if (masked) {
 #pragma unroll
-                    for (int i = 0; i < kCols; ++i)
-                        if (key > rows.last[c0 + i] || key < rows.first[c0 + i])
+                    for (int i = 0; i < kSub; ++i)
+                        if (key > rows.last[cb + i] || key < rows.first[cb + i])
                             x[i] = -CUDART_INF_F;
                 }
             };
 
             wait(&tl.s_full[g & 1], (g >> 1) & 1);
             ptx::tc_fence_after();
-            exponents(false);
-            float top = x[0];
+            // With more than kSub columns the exponents are computed again
+            // below: holding them took registers that spilled (64 rows: 290
+            // bytes a thread, whose reloads missed the small L1).
+            float x[kSub];
+            float top = -CUDART_INF_F;
 #pragma unroll
-            for (int i = 1; i + 1 < kCols; i += 2) top = ptx::max3(top, x[i], x[i + 1]);
-            top = fmaxf(top, x[kCols - 1]);
+            for (int b = 0; b < kCols / kSub; ++b) {
+                exponents(x, b, false);
+#pragma unroll
+                for (int i = 0; i < kSub; i += 2) top = ptx::max3(top, x[i], x[i + 1]);
+            }
             if (group_any(bar_id, top > kBias<kE> + kSlack<kE>)) {
                 // Some weight is too large for its row's unit: raise the units.
-                exponents(true);
                 float mine = 0.f;
 #pragma unroll
-                for (int i = 0; i < kCols; ++i) {
-                    const float m = warp_max(x[i]);
-                    if (lane == i) mine = m;
+                for (int b = 0; b < kCols / kSub; ++b) {
+                    exponents(x, b, true);
+#pragma unroll
+                    for (int i = 0; i < kSub; ++i) {
+                        const float m = warp_max(x[i]);
+                        if (lane == b * kSub + i) mine = m;
+                    }
                 }
                 if (lane < kCols) tl.wmax[quarter][c0 + lane] = mine;
                 group_sync(bar_id);
@@ -859,32 +886,36 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
                     }
                 }
                 if (j > 0) ptx::tmem_wait_st();
-                exponents(false);
+                if (kCols == kSub) exponents(x, 0, false);
             }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&tl.s_free[g & 1]));
+            auto scores_read = [&]() {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&tl.s_free[g & 1]));
+            };
+            if (kCols == kSub) scores_read();
 
             // The products that read P last must be done.
             if (g > 0) wait(&tl.pv_done, (g - 1) & 1);
-            const uint64_t inv2 = ptx::f2_pack(inv_vs, inv_vs);
+            const uint64_t inv2 = ptx::f2_pack(sc.z, sc.z);
 #pragma unroll
             for (int b = 0; b < kCols / kSub; ++b) {
-                float w[kSub];
+                if (kCols > kSub) exponents(x, b, false);
 #pragma unroll
                 for (int i = 0; i < kSub; i += 2) {
-                    w[i] = ptx::ex2(x[b * kSub + i]);
-                    w[i + 1] = ptx::ex2(x[b * kSub + i + 1]);
+                    x[i] = ptx::ex2(x[i]);
+                    x[i + 1] = ptx::ex2(x[i + 1]);
                     uint64_t& sum = l[(b * kSub + i) / 2];
-                    const uint64_t w2 = ptx::f2_pack(w[i], w[i + 1]);
+                    const uint64_t w2 = ptx::f2_pack(x[i], x[i + 1]);
                     sum = kE ? ptx::f2_fma(w2, inv2, sum) : ptx::f2_add(w2, sum);
                 }
-                if (kE && zero) {
+                if (kE && sc.w != 0.f) {  // V is zero there; its weights stay in l
 #pragma unroll
-                    for (int i = 0; i < kSub; ++i) w[i] = 0.f;
+                    for (int i = 0; i < kSub; ++i) x[i] = 0.f;
                 }
-                store_weights<kE, kR>(w, p_row, r & 7, c0 + b * kSub);
+                store_weights<kE, kR>(x, p_row, r & 7, c0 + b * kSub);
             }
+            if (kCols > kSub) scores_read();
             if (key0 + 127 >= it.r.end) {
                 // Slots past the end hold anything: zero them before 0 * NaN.
                 // V's tile in the ring: K0, then K(j+1), V(j) in turn.
@@ -988,7 +1019,7 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
         c = next;
         it = next_it;
     }
-    if (threadIdx.x == 0 && !tail_part) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (threadIdx.x == 0 && !tail_part && !p.whole) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
 }
 
 template <bool kE, int kR>
@@ -1015,6 +1046,7 @@ __global__ void __launch_bounds__(Shape<kE, kR>::kThreads, Shape<kE, kR>::kCtasP
             ptx::mbar_init(ptx::smem_u32(&tl.s_full[i]), 1);
             ptx::mbar_init(ptx::smem_u32(&tl.s_free[i]), kSoftWarps);
         }
+        for (int i = 0; i < 4; ++i) ptx::mbar_init(ptx::smem_u32(&tl.scales_full[i]), 1);
         ptx::mbar_init(ptx::smem_u32(&tl.p_full), kSoftWarps);
         ptx::mbar_init(ptx::smem_u32(&tl.pv_done), 1);
         ptx::mbar_init(ptx::smem_u32(&tl.drain), 1);
