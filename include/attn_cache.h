@@ -171,7 +171,7 @@ int attn_fwd_cache(const attn_cache_t* cache, const void* q, void* o, float* lse
 
 /* Device workspace bytes that attn_fwd_cache needs on the current device (0
  * on bad sizes or without a device).  It grows with h_q / h_kv * max_seqlen_q
- * up to 64 rows and not beyond. */
+ * and is the same for all above 32 rows. */
 size_t attn_fwd_cache_workspace_bytes(int h_q, int h_kv, int max_seqlen_q);
 
 #ifdef __cplusplus

@@ -7,6 +7,7 @@
 #include "attn_cache.h"
 #include "attn_cache_append.cuh"
 #include "attn_cache_kernel.cuh"
+#include "attn_cache_wide.cuh"
 
 namespace {
 
@@ -20,19 +21,19 @@ int init_cache_device(int dev, DeviceState** st) {
     std::lock_guard<std::mutex> lock(g_mutex);
     if (ready[dev]) return ATTN_OK;
     const auto smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
-#define SDPA10_CACHE_SMEM(kE, kR)                                                  \
-    if (cudaFuncSetAttribute(cache::attn_fwd_cache_kernel<kE, kR>, smem,           \
-                             cache::Shape<kE, kR>::kAlloc) != cudaSuccess)         \
-    return ATTN_ERR_CUDA
-    SDPA10_CACHE_SMEM(false, 8);
-    SDPA10_CACHE_SMEM(false, 16);
-    SDPA10_CACHE_SMEM(false, 32);
-    SDPA10_CACHE_SMEM(false, 64);
-    SDPA10_CACHE_SMEM(true, 8);
-    SDPA10_CACHE_SMEM(true, 16);
-    SDPA10_CACHE_SMEM(true, 32);
-    SDPA10_CACHE_SMEM(true, 64);
-#undef SDPA10_CACHE_SMEM
+    const auto allow = [&](const void* kernel, int bytes) {
+        return cudaFuncSetAttribute(kernel, smem, bytes) == cudaSuccess;
+    };
+    using namespace cache;
+    if (!allow((const void*)attn_fwd_cache_kernel<false, 8>, Shape<false, 8>::kAlloc) ||
+        !allow((const void*)attn_fwd_cache_kernel<false, 16>, Shape<false, 16>::kAlloc) ||
+        !allow((const void*)attn_fwd_cache_kernel<false, 32>, Shape<false, 32>::kAlloc) ||
+        !allow((const void*)attn_fwd_cache_wide_kernel<false>, WideShape<false>::kAlloc) ||
+        !allow((const void*)attn_fwd_cache_kernel<true, 8>, Shape<true, 8>::kAlloc) ||
+        !allow((const void*)attn_fwd_cache_kernel<true, 16>, Shape<true, 16>::kAlloc) ||
+        !allow((const void*)attn_fwd_cache_kernel<true, 32>, Shape<true, 32>::kAlloc) ||
+        !allow((const void*)attn_fwd_cache_wide_kernel<true>, WideShape<true>::kAlloc))
+        return ATTN_ERR_CUDA;
     ready[dev] = true;
     return ATTN_OK;
 }
@@ -94,21 +95,22 @@ bool encode_pool(CUtensorMap* m, const attn_cache_t* c, void* base, int box) {
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Query rows of a tile: the smallest of 8, 16, 32 and 64 that holds a
-// sequence's rows of one key/value head.
+// Query rows of a tile: the smallest of 8, 16 and 32 that holds a sequence's
+// rows of one key/value head, else 128 (the wide kernel).
 int cache_rows(int group, int max_seqlen) {
     const long long rows = static_cast<long long>(group) * max_seqlen;
-    return rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : 64));
+    return rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : 128));
 }
 
-constexpr int kWholeTiles = 4;      // see attn_fwd_cache
-constexpr int kCacheCtasPerSm = 2;  // of any variant, at most
+constexpr int kWholeTiles = 4;  // see attn_fwd_cache
 
+// The parts that a launch may leave: two for each CTA, of which the narrow
+// kernel has up to two on an SM.
 struct CacheWorkspace {
     size_t ml, o, bytes;  // offsets; the shares' records come first
 };
 CacheWorkspace cache_workspace(int sms, int rows) {
-    const size_t ctas = static_cast<size_t>(sms) * kCacheCtasPerSm;
+    const size_t ctas = static_cast<size_t>(sms) * (rows > cache::kNarrowRows ? 1 : 2);
     CacheWorkspace w;
     w.ml = round_up(ctas * sizeof(int4), 256);
     w.o = w.ml + round_up(ctas * 2 * rows * sizeof(float2), 256);
@@ -134,15 +136,16 @@ cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <bool kE, int kR>
-int launch_fwd_cache(const CUtensorMap& tk, const CUtensorMap& tv, const cache::FwdCacheParams& p,
+template <class S, int kR>
+int launch_fwd_cache(void (*kernel)(const CUtensorMap, const CUtensorMap,
+                                    const cache::FwdCacheParams),
+                     const CUtensorMap& tk, const CUtensorMap& tv, const cache::FwdCacheParams& p,
                      int sms, long long most_units, cudaStream_t cs) {
-    using S = cache::Shape<kE, kR>;
-    static_assert(S::kCtasPerSm <= kCacheCtasPerSm, "the workspace holds a part of each CTA");
+    static_assert(S::kCtasPerSm <= (kR > cache::kNarrowRows ? 1 : 2),
+                  "the workspace holds two parts of each CTA");
     const long long all = static_cast<long long>(sms) * S::kCtasPerSm;
     const unsigned grid = static_cast<unsigned>(most_units < all ? most_units : all);
-    if (launch_after(cache::attn_fwd_cache_kernel<kE, kR>, dim3(grid), S::kThreads, S::kAlloc, cs,
-                     tk, tv, p) != cudaSuccess)
+    if (launch_after(kernel, dim3(grid), S::kThreads, S::kAlloc, cs, tk, tv, p) != cudaSuccess)
         return ATTN_ERR_CUDA;
     g_last_launches = 1;
     if (p.whole) return ATTN_OK;
@@ -151,6 +154,24 @@ int launch_fwd_cache(const CUtensorMap& tk, const CUtensorMap& tv, const cache::
         return ATTN_ERR_CUDA;
     g_last_launches = 2;
     return ATTN_OK;
+}
+
+template <bool kE>
+int launch_fwd_cache_rows(int rows, const CUtensorMap& tk, const CUtensorMap& tv,
+                          const cache::FwdCacheParams& p, int sms, long long most,
+                          cudaStream_t cs) {
+    using namespace cache;
+    if (rows == 8)
+        return launch_fwd_cache<Shape<kE, 8>, 8>(attn_fwd_cache_kernel<kE, 8>, tk, tv, p, sms,
+                                                 most, cs);
+    if (rows == 16)
+        return launch_fwd_cache<Shape<kE, 16>, 16>(attn_fwd_cache_kernel<kE, 16>, tk, tv, p, sms,
+                                                   most, cs);
+    if (rows == 32)
+        return launch_fwd_cache<Shape<kE, 32>, 32>(attn_fwd_cache_kernel<kE, 32>, tk, tv, p, sms,
+                                                   most, cs);
+    return launch_fwd_cache<WideShape<kE>, 128>(attn_fwd_cache_wide_kernel<kE>, tk, tv, p, sms,
+                                                most, cs);
 }
 
 }  // namespace
@@ -338,14 +359,7 @@ extern "C" int attn_fwd_cache(const attn_cache_t* c, const void* q, void* o, flo
     const long long most = p.whole ? row_tiles : row_tiles * key_tiles;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const int sms = st->num_sms;
-    if (c->type == ATTN_CACHE_E4M3) {
-        if (rows == 8) return launch_fwd_cache<true, 8>(tk, tv, p, sms, most, cs);
-        if (rows == 16) return launch_fwd_cache<true, 16>(tk, tv, p, sms, most, cs);
-        if (rows == 32) return launch_fwd_cache<true, 32>(tk, tv, p, sms, most, cs);
-        return launch_fwd_cache<true, 64>(tk, tv, p, sms, most, cs);
-    }
-    if (rows == 8) return launch_fwd_cache<false, 8>(tk, tv, p, sms, most, cs);
-    if (rows == 16) return launch_fwd_cache<false, 16>(tk, tv, p, sms, most, cs);
-    if (rows == 32) return launch_fwd_cache<false, 32>(tk, tv, p, sms, most, cs);
-    return launch_fwd_cache<false, 64>(tk, tv, p, sms, most, cs);
+    return c->type == ATTN_CACHE_E4M3
+               ? launch_fwd_cache_rows<true>(rows, tk, tv, p, sms, most, cs)
+               : launch_fwd_cache_rows<false>(rows, tk, tv, p, sms, most, cs);
 }

@@ -1,7 +1,8 @@
 // attn_cache_kernel.cuh -- attention of a packed batch of queries over a paged
 // key/value cache (BF16, or E4M3 with a scale for each page and head).
 //
-// For few query rows over many keys the work is reading the cache once, so the
+// For few query rows (up to 32 of a key/value head; attn_cache_wide.cuh has the
+// kernel for more) over many keys the work is reading the cache once, so the
 // products are laid out with the keys and the head dim on the 128 rows of the
 // tensor core's tile and the query rows on its narrow side:
 //     S^T [128 keys x R rows] = K Q^T        (A = K tile,   B = Q)
@@ -39,7 +40,7 @@
 namespace sdpa10 {
 namespace cache {
 
-constexpr int kMaxRows = 64;       // query rows of the widest tile
+constexpr int kNarrowRows = 32;    // widest tile of this file's kernel
 // log2 of a row's unit of weights, and of how far a weight may pass it before
 // the unit is raised.  E4M3 pages: 2^11 p stays below 2^15 in FP16 and E5M2,
 // and the smallest E5M2 number is 2^-27 of the unit.
@@ -264,69 +265,58 @@ __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
 
 // ------------------------------------------------------------------ layout
 // kE: E4M3 pages.  kR: query rows of a tile.
-template <bool kE, int kR>
+template <bool kE_, int kR>
 struct Shape {
+    static constexpr bool kE = kE_;
     static constexpr int kN = kR < 16 ? 16 : kR;          // the MMA's narrow side
-    static constexpr int kGroups = kR > 32 ? 2 : 1;       // column groups of four softmax warps
-    static constexpr int kCols = kR / kGroups;            // columns of a thread
-    static constexpr int kSub = kCols < 16 ? kCols : 16;  // columns worked on at a time
-    static constexpr int kSoftThreads = 128 * kGroups;
-    static constexpr int kThreads = kSoftThreads + 64;
+    static constexpr int kSub = kR < 16 ? kR : 16;        // columns worked on at a time
+    static constexpr int kThreads = 128 + 64;
     static constexpr int kQPieces = kE ? 2 : 1, kPPieces = kE ? 3 : 1;
     static constexpr int kElem = kE ? 1 : 2;
     static constexpr int kTile = 128 * kHeadDim * kElem;  // a K or V tile
     static constexpr int kQPiece = kN * kHeadDim * kElem;
-    // P: rows of 128 bytes, one per key.  Piece i of E4M3 starts kN bytes after
-    // the one before; three of 64 columns need a second buffer.
-    static constexpr int kPBuf = 128 * 128;
-    static constexpr int kPBytes = (kPPieces * kN * kElem > 128 ? 2 : 1) * kPBuf;
+    // P: rows of 128 bytes, one per key; E4M3's pieces side by side.
+    static constexpr int kPBytes = 128 * 128;
+    static_assert(kPPieces * kN * kElem <= 128, "a key's weights are one row");
     static constexpr int kOffQ = 0;
     static constexpr int kOffP = kOffQ + (kQPieces * kQPiece + 1023) / 1024 * 1024;
     static constexpr int kOffRing = kOffP + kPBytes;
-    static constexpr int kTail = 5632;  // barriers and the small arrays below
+    static constexpr int kTail = 4608;  // barriers and the small arrays below
     // Two CTAs of an SM overlap one's softmax with the other's products.  Ring
     // and P of BF16 pages leave room for one, whose deeper ring has the same
     // bytes in flight.
     static constexpr int kCtasPerSm = kE ? 2 : 1;
     static constexpr int kBudget = (kE ? 113 : 227) * 1024 - 1024;
     static constexpr int kSlots = (kBudget - kOffRing - kTail) / kTile;
+    static constexpr int kScaleTiles = 4;
     static_assert(kSlots >= 3 && kSlots <= 8, "the ring needs K(j+1) beside K(j) and V(j)");
-    // The scales of tile g + 4 are written over those of tile g once a slot is
-    // free for K(g+4); then V(g), kSlots tiles before it, has been used.
-    static_assert(!kE || kSlots <= 5, "four tiles' scales are kept");
     static constexpr int kOffTail = kOffRing + kSlots * kTile;
     static constexpr int kAlloc = kOffTail + kTail + 1024;
     // The pieces of P side by side are one product of 3 kN columns, of which
     // the epilogue adds three (an MMA of N columns takes 32 + N / 4 cycles here,
-    // N = 16 38, so four of 48 columns take 174 where twelve of 16 take 460);
-    // 64 rows leave no Tensor Memory for that and add up in place.
-    static constexpr bool kSideBySide = kE && kN <= 32;
-    static constexpr int kPN = kSideBySide ? 3 * kN : kN;  // columns of one product with V
+    // N = 16 38, so four of 48 columns take 174 where twelve of 16 take 460).
+    static constexpr int kPN = kPPieces * kN;  // columns of one product with V
     static constexpr int kCols0 = 2 * kN + kPN;
     static constexpr uint32_t kTmemCols = kCols0 <= 64 ? 64 : (kCols0 <= 128 ? 128 : 256);
-    __host__ __device__ static constexpr int p_offset(int piece) {
-        const int at = piece * kN * kElem;
-        return at + kN * kElem <= 128 ? at : kPBuf + at - 128;
-    }
 };
 
+template <int kRows>
 struct __align__(16) Rows {
-    float scale[kMaxRows];   // of the row's scores: scale log2(e), E4M3: times 2^-e of its Q
-    float offset[kMaxRows];  // bias - M of the row, kFresh while it has seen no key
-    int last[kMaxRows];      // last key the row sees
-    int first[kMaxRows];     // first one
-    int row[kMaxRows];       // query * h_q + head; -1: no such row
+    float scale[kRows];   // of the row's scores: scale log2(e), E4M3: times 2^-e of its Q
+    float offset[kRows];  // bias - M of the row, kFresh while it has seen no key
+    int last[kRows];      // last key the row sees
+    int first[kRows];     // first one
+    int row[kRows];       // query * h_q + head; -1: no such row
 };
 
-struct Tail {
-    Rows rows[2];  // of this item and the next
-    float wmax[4][kMaxRows];
-    float alpha[kMaxRows];
-    // Scales of the last tiles' boxes (E4M3): K's, log2 of V's, 1 / V's, V's is 0.
-    float4 scales[4][16];
-    uint64_t scales_full[4];
+// What the roles share: the schedule, the ring and the E4M3 scales.
+template <int kScaleTiles>
+struct Shared {
+    // Scales of the last tiles' boxes: K's, log2 of V's, 1 / V's, V's is 0.
+    float4 scales[kScaleTiles][16];
+    uint64_t scales_full[kScaleTiles];
     uint64_t full[8], empty[8];
-    uint64_t q_full, s_full[2], s_free[2], p_full, pv_done, drain;
+    uint64_t q_full, s_full[3], s_free[2], p_full, pv_done[2], drain;
     long long begin;  // first unit of this share
     long long wsum[16];
     uint32_t tmem;
@@ -334,11 +324,17 @@ struct Tail {
     Cursor cursor;
     int chunk;  // units of every share
 };
-static_assert(sizeof(Tail) <= 5632, "");
+
+struct Tail : Shared<4> {
+    Rows<kNarrowRows> rows[2];  // of this item and the next
+    float wmax[4][kNarrowRows];
+    float alpha[kNarrowRows];
+};
+static_assert(sizeof(Tail) <= 4608, "");
 
 // Where this CTA's share of the units begins (every thread of the CTA calls).
-template <int kThreads>
-__device__ __forceinline__ void find_share(const FwdCacheParams& p, Tail& tl) {
+template <int kThreads, class T>
+__device__ __forceinline__ void find_share(const FwdCacheParams& p, T& tl) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per_seq = p.h_kv * p.head_tiles;
     constexpr int kWarps = kThreads / 32;
@@ -413,11 +409,16 @@ __device__ __forceinline__ void find_share(const FwdCacheParams& p, Tail& tl) {
 // ------------------------------------------------------------------ producer
 // One warp: lane i loads the tile's i-th box (a run of keys of one page), and
 // with E4M3 pages keeps the box's scales one tile ahead and its page two.
-template <bool kE, int kR>
+template <class S, class T>
 __device__ __forceinline__ void producer_role(const FwdCacheParams& p, const CUtensorMap* tm_k,
-                                              const CUtensorMap* tm_v, Tail& tl, uint32_t ring,
+                                              const CUtensorMap* tm_v, T& tl, uint32_t ring,
                                               const WaitCtx& wc, int lane) {
-    using S = Shape<kE, kR>;
+    constexpr bool kE = S::kE;
+    // The scales of tile g + kScaleTiles are written over those of tile g once
+    // a slot is free for its K, 2 (g + kScaleTiles) - 1 tiles into the ring;
+    // then V(g), at most the (2 g + 2)-th, has been used.
+    static_assert(!kE || S::kSlots <= 2 * S::kScaleTiles - 3, "scales kept too short");
+    constexpr uint32_t kKeep = S::kScaleTiles - 1;
     const int boxes = 128 / p.box;
     const uint32_t box_bytes = static_cast<uint32_t>(p.box) * 128u;  // of one 128-byte column
     uint32_t loads = 0, g = 0;
@@ -472,11 +473,11 @@ __device__ __forceinline__ void producer_role(const FwdCacheParams& p, const CUt
             if constexpr (kE) {
                 if (lane < 16) {
                     const float lv = fminf(fmaxf(__log2f(vs), -64.f), 64.f);
-                    tl.scales[g & 3][lane] =
+                    tl.scales[g & kKeep][lane] =
                         make_float4(ks, lv, ptx::ex2(-lv), vs >= 0x1p-64f ? 0.f : 1.f);
                 }
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&tl.scales_full[g & 3]));
+                if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&tl.scales_full[g & kKeep]));
                 ++g;
             }
             return true;
@@ -561,17 +562,14 @@ __device__ __forceinline__ void mma_role(const FwdCacheParams& p, Tail& tl, uint
             desc_lo_sw128(ring + (used % S::kSlots) * S::kTile, kE ? S::kTile : 16384);
         constexpr int kSteps = kE ? 4 : 8, kStepBytes = kE ? 4096 : 2048;
 #pragma unroll
-        for (int i = 0; i < (S::kSideBySide ? 1 : S::kPPieces); ++i)
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k) {
-                const uint64_t a = desc_from_lo(va + ((k * kStepBytes) >> 4));
-                const uint64_t b = desc_from_lo(desc_lo_sw128(sp + S::p_offset(i), 16384) +
-                                                ((k * kStepBytes) >> 4));
-                const uint32_t acc = accumulate || i + k > 0 ? 1u : 0u;
-                if constexpr (kE) mma_f8_warp(o_tm, a, b, kIdPV, acc);
-                else ptx::mma_ss_warp(o_tm, a, b, kIdPV, acc);
-            }
-        ptx::mma_commit_warp(ptx::smem_u32(&tl.pv_done));
+        for (int k = 0; k < kSteps; ++k) {
+            const uint64_t a = desc_from_lo(va + ((k * kStepBytes) >> 4));
+            const uint64_t b = desc_from_lo(desc_lo_sw128(sp, 16384) + ((k * kStepBytes) >> 4));
+            const uint32_t acc = accumulate || k > 0 ? 1u : 0u;
+            if constexpr (kE) mma_f8_warp(o_tm, a, b, kIdPV, acc);
+            else ptx::mma_ss_warp(o_tm, a, b, kIdPV, acc);
+        }
+        ptx::mma_commit_warp(ptx::smem_u32(&tl.pv_done[0]));
         ptx::mma_commit_warp(ptx::smem_u32(&tl.empty[used % S::kSlots]));
         ++used;
         ++pv;
@@ -616,41 +614,31 @@ __device__ __forceinline__ float lane_sums(float (&v)[kC], int lane) {
     return r;
 }
 
-// The queries of an item's rows [c0, c0 + kCols) into shared memory, and what
-// the rows see.  128 threads.
-template <bool kE, int kR>
-__device__ __forceinline__ void load_rows(const FwdCacheParams& p, Rows& rows, uint8_t* sq,
-                                          const Item& it, int h, int c0, int r) {
-    using S = Shape<kE, kR>;
+// Rows kRows of an item's queries into shared memory as operands (E4M3: two
+// pieces, `piece` bytes apart; BF16: two halves, `piece` bytes apart), and the
+// factors of their scores.  kThreads threads.
+template <bool kE, int kRows, int kThreads>
+__device__ __forceinline__ void load_queries(const FwdCacheParams& p, float* scale, uint8_t* sq,
+                                             int piece, const Item& it, int h, int tid) {
     const int kv_head = h / p.head_tiles;
     const int head0 = (h - kv_head * p.head_tiles) * p.heads_per_tile;  // in the group
     const int heads = min(p.heads_per_tile, p.group - head0);
     const int queries = it.r.i1 - it.r.i0 + 1;
-    const int shift = it.s.len - it.s.n;
-    uint4 w[S::kCols / 8];
+    constexpr int kEach = kRows * 16 / kThreads;  // 16-byte parts of a thread
+    uint4 w[kEach];
 #pragma unroll
-    for (int k = 0; k < S::kCols / 8; ++k) {
-        const int c = c0 + k * 8 + (r >> 4);
+    for (int k = 0; k < kEach; ++k) {
+        const int c = (k * kThreads + tid) >> 4;
         const int qi = p.div_heads.div(c), e = c - qi * p.heads_per_tile;
         w[k] = make_uint4(0, 0, 0, 0);
         if (qi < queries && e < heads)
             w[k] = reinterpret_cast<const uint4*>(
                 p.q + static_cast<long long>(it.s.row0 + it.r.i0 + qi) * p.q_stride +
-                (kv_head * p.group + head0 + e) * kHeadDim)[r & 15];
-    }
-    if (r < S::kCols) {
-        const int c = c0 + r;
-        const int qi = p.div_heads.div(c), e = c - qi * p.heads_per_tile;
-        const bool there = qi < queries && e < heads;
-        const int i = it.r.i0 + qi;
-        rows.row[c] = there ? (it.s.row0 + i) * p.h_q + kv_head * p.group + head0 + e : -1;
-        rows.last[c] = !there ? -1 : (p.causal ? min(it.s.kv - 1, shift + i) : it.s.kv - 1);
-        rows.first[c] = there && p.window >= 0 ? shift + i - p.window : 0;
-        rows.offset[c] = kFresh;
+                (kv_head * p.group + head0 + e) * kHeadDim)[tid & 15];
     }
 #pragma unroll
-    for (int k = 0; k < S::kCols / 8; ++k) {
-        const int c = c0 + k * 8 + (r >> 4), part = r & 15;
+    for (int k = 0; k < kEach; ++k) {
+        const int c = (k * kThreads + tid) >> 4, part = tid & 15;
         if constexpr (kE) {
             float x[8];
             const uint32_t v[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
@@ -666,8 +654,7 @@ __device__ __forceinline__ void load_rows(const FwdCacheParams& p, Rows& rows, u
             const int ex = min(max(static_cast<int>(__float_as_uint(top) >> 23), 20), 250);
             const float up = __uint_as_float(static_cast<uint32_t>(261 - ex) << 23);
             if (part == 0)
-                rows.scale[c] =
-                    p.scale_log2 * __uint_as_float(static_cast<uint32_t>(ex - 7) << 23);
+                scale[c] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(ex - 7) << 23);
             uint32_t hi[2], lo[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -680,12 +667,54 @@ __device__ __forceinline__ void load_rows(const FwdCacheParams& p, Rows& rows, u
             }
             uint8_t* at = sq + c * 128 + (((part >> 1) ^ (c & 7)) << 4) + (part & 1) * 8;
             *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(at + S::kQPiece) = make_uint2(lo[0], lo[1]);
+            *reinterpret_cast<uint2*>(at + piece) = make_uint2(lo[0], lo[1]);
         } else {
-            *reinterpret_cast<uint4*>(sq + (part >> 3) * S::kN * 128 + c * 128 +
+            *reinterpret_cast<uint4*>(sq + (part >> 3) * piece + c * 128 +
                                       (((part & 7) ^ (c & 7)) << 4)) = w[k];
         }
     }
+}
+
+// What row c of an item's tile is and sees.
+struct RowView {
+    int row;          // query * h_q + head; -1: no such row
+    int first, last;  // keys
+};
+__device__ __forceinline__ RowView row_view(const FwdCacheParams& p, const Item& it, int h, int c) {
+    const int kv_head = h / p.head_tiles;
+    const int head0 = (h - kv_head * p.head_tiles) * p.heads_per_tile;
+    const int qi = p.div_heads.div(c), e = c - qi * p.heads_per_tile;
+    const int i = it.r.i0 + qi, shift = it.s.len - it.s.n;
+    RowView v;
+    v.row = -1;
+    v.last = -1;
+    v.first = 0;
+    if (i <= it.r.i1 && e < p.group - head0) {
+        v.row = (it.s.row0 + i) * p.h_q + kv_head * p.group + head0 + e;
+        v.last = p.causal ? min(it.s.kv - 1, shift + i) : it.s.kv - 1;
+        if (p.window >= 0) v.first = shift + i - p.window;
+    }
+    return v;
+}
+
+// A weight's three E5M2 numbers: FP16 values w (two words of two) are cut into
+// runs of three significant bits, the last one rounded; piece[i] gets the
+// four bytes of run i.
+__device__ __forceinline__ void split_weights(float a, float b, float c, float d, uint32_t& hi,
+                                              uint32_t& mid, uint32_t& lo) {
+    uint32_t h[2], m[2], l[2];
+    const __half2 w[2] = {__floats2half2_rn(a, b), __floats2half2_rn(c, d)};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(&w[j]);
+        h[j] = v & 0xff00ff00u;
+        const uint32_t rest = hsub2(v, h[j]);
+        m[j] = rest & 0xff00ff00u;
+        l[j] = hsub2(rest, m[j]) + 0x00800080u;  // half of its last place
+    }
+    hi = prmt(h[0], h[1], 0x7531);
+    mid = prmt(m[0], m[1], 0x7531);
+    lo = prmt(l[0], l[1], 0x7531);
 }
 
 // A thread's weights of kSub columns into its row of P.
@@ -693,36 +722,22 @@ template <bool kE, int kR>
 __device__ __forceinline__ void store_weights(const float (&w)[Shape<kE, kR>::kSub], uint32_t row,
                                               int x, int c) {
     using S = Shape<kE, kR>;
-    auto at = [&](int byte) -> uint32_t {  // byte of the row (both buffers), swizzled
-        return row + (byte >> 7) * S::kPBuf + ((((byte & 127) >> 4) ^ x) << 4) + (byte & 15);
+    auto at = [&](int byte) -> uint32_t {  // byte of the row, swizzled
+        return row + (((byte >> 4) ^ x) << 4) + (byte & 15);
     };
     if constexpr (kE) {
         uint32_t piece[3][S::kSub / 4];
 #pragma unroll
-        for (int i = 0; i < S::kSub / 4; ++i) {
-            uint32_t hi[2], mid[2], lo[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const __half2 h = __floats2half2_rn(w[4 * i + 2 * j], w[4 * i + 2 * j + 1]);
-                const uint32_t v = *reinterpret_cast<const uint32_t*>(&h);
-                hi[j] = v & 0xff00ff00u;
-                const uint32_t rest = hsub2(v, hi[j]);
-                mid[j] = rest & 0xff00ff00u;
-                // The last piece is rounded (half of its last place added).
-                lo[j] = hsub2(rest, mid[j]) + 0x00800080u;
-            }
-            piece[0][i] = prmt(hi[0], hi[1], 0x7531);
-            piece[1][i] = prmt(mid[0], mid[1], 0x7531);
-            piece[2][i] = prmt(lo[0], lo[1], 0x7531);
-        }
+        for (int i = 0; i < S::kSub / 4; ++i)
+            split_weights(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3], piece[0][i],
+                          piece[1][i], piece[2][i]);
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
-            const int byte = (S::p_offset(i) >= S::kPBuf ? 128 + S::p_offset(i) - S::kPBuf
-                                                         : S::p_offset(i)) + c;
             if constexpr (S::kSub == 16)
-                ptx::st_shared_v4(at(byte), piece[i][0], piece[i][1], piece[i][2], piece[i][3]);
+                ptx::st_shared_v4(at(i * S::kN + c), piece[i][0], piece[i][1], piece[i][2],
+                                  piece[i][3]);
             else
-                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at(byte)),
+                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at(i * S::kN + c)),
                              "r"(piece[i][0]), "r"(piece[i][1])
                              : "memory");
         }
@@ -736,22 +751,18 @@ __device__ __forceinline__ void store_weights(const float (&w)[Shape<kE, kR>::kS
     }
 }
 
-// Four warps and kCols columns: thread r holds key r of the tile, and Tensor
-// Memory lane r.  A wait that gives up sets `dead`: the warp then goes through
+// Four warps: thread r holds key r of the tile, and Tensor Memory lane r.  A wait that gives up sets `dead`: the warp then goes through
 // its tiles without waiting (it keeps the group's barriers in step) and the
 // results are unspecified.
 template <bool kE, int kR>
 __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, uint8_t* sq,
                                              uint32_t sp, uint8_t* ring, uint32_t tmem,
-                                             const WaitCtx& wc, int group) {
+                                             const WaitCtx& wc) {
     using S = Shape<kE, kR>;
-    constexpr int kCols = S::kCols, kSub = S::kSub, kPairs = kCols / 2;
-    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
-    const int r = quarter * 32 + lane;
-    const int c0 = S::kGroups > 1 ? group * kCols : 0;
-    const int bar_id = 1 + group;
+    constexpr int kCols = kR, kSub = S::kSub, kPairs = kCols / 2, bar_id = 1;
+    const int r = threadIdx.x, lane = r & 31, quarter = r >> 5;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t s_tm = tmem + lanes + c0, o_tm = tmem + lanes + 2 * S::kN + c0;
+    const uint32_t s_tm = tmem + lanes, o_tm = tmem + lanes + 2 * S::kN;
     const uint32_t p_row = sp + r * 128;
     const int box_log2 = 31 - __clz(p.box);
     uint32_t g = 0, used = 0, items = 0;
@@ -760,7 +771,15 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
         if (!dead && !wait_bar_warp(ptx::smem_u32(bar), parity, wc)) dead = true;
     };
     auto stage = [&](const Item& it, int h) {
-        load_rows<kE, kR>(p, tl.rows[items & 1], sq, it, h, c0, r);
+        Rows<kNarrowRows>& rows = tl.rows[items & 1];
+        load_queries<kE, kR, 128>(p, rows.scale, sq, kE ? S::kQPiece : S::kN * 128, it, h, r);
+        if (r < kCols) {
+            const RowView v = row_view(p, it, h, r);
+            rows.row[r] = v.row;
+            rows.first[r] = v.first;
+            rows.last[r] = v.last;
+            rows.offset[r] = kFresh;
+        }
         ptx::fence_proxy_async_smem();
         group_sync(bar_id);
         if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&tl.q_full));
@@ -774,7 +793,7 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
         stage(it, c.h);
     }
     while (c.left > 0) {
-        Rows& rows = tl.rows[items & 1];
+        Rows<kNarrowRows>& rows = tl.rows[items & 1];
         const int head = c.h / p.head_tiles;
         const int shift = it.s.len - it.s.n;
         const int min_last = p.causal ? min(it.s.kv - 1, shift + it.r.i0) : it.s.kv - 1;
@@ -797,7 +816,7 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
             // Of kSub columns; `absolute`: without the offset.
             auto exponents = [&](float (&x)[kSub], int b, bool absolute) {
                 tmem_load(s_at + b * kSub, x);
-                const int cb = c0 + b * kSub;
+                const int cb = b * kSub;
 #pragma unroll
                 for (int i = 0; i < kSub; i += 4) {
                     const float4 o = absolute ? make_float4(0.f, 0.f, 0.f, 0.f)
@@ -824,9 +843,8 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
 
             wait(&tl.s_full[g & 1], (g >> 1) & 1);
             ptx::tc_fence_after();
-            // With more than kSub columns the exponents are computed again
-            // below: holding them took registers that spilled (64 rows: 290
-            // bytes a thread, whose reloads missed the small L1).
+            // With more than kSub columns the exponents are computed again below
+            // instead of held.
             float x[kSub];
             float top = -CUDART_INF_F;
 #pragma unroll
@@ -847,10 +865,10 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
                         if (lane == b * kSub + i) mine = m;
                     }
                 }
-                if (lane < kCols) tl.wmax[quarter][c0 + lane] = mine;
+                if (lane < kCols) tl.wmax[quarter][lane] = mine;
                 group_sync(bar_id);
                 if (r < kCols) {
-                    const int col = c0 + r;
+                    const int col = r;
                     const float m = fmaxf(fmaxf(tl.wmax[0][col], tl.wmax[1][col]),
                                           fmaxf(tl.wmax[2][col], tl.wmax[3][col]));
                     const float old = rows.offset[col];
@@ -862,14 +880,14 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
                 }
                 group_sync(bar_id);
                 if (j > 0) {
-                    wait(&tl.pv_done, (g - 1) & 1);
+                    wait(&tl.pv_done[0], (g - 1) & 1);
                     ptx::tc_fence_after();
                 }
 #pragma unroll
                 for (int b = 0; b < kCols / 8; ++b) {
                     float a[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) a[i] = tl.alpha[c0 + 8 * b + i];
+                    for (int i = 0; i < 8; ++i) a[i] = tl.alpha[8 * b + i];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         l[4 * b + i] = ptx::f2_mul(l[4 * b + i],
@@ -896,7 +914,7 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
             if (kCols == kSub) scores_read();
 
             // The products that read P last must be done.
-            if (g > 0) wait(&tl.pv_done, (g - 1) & 1);
+            if (g > 0) wait(&tl.pv_done[0], (g - 1) & 1);
             const uint64_t inv2 = ptx::f2_pack(sc.z, sc.z);
 #pragma unroll
             for (int b = 0; b < kCols / kSub; ++b) {
@@ -913,7 +931,7 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
 #pragma unroll
                     for (int i = 0; i < kSub; ++i) x[i] = 0.f;
                 }
-                store_weights<kE, kR>(x, p_row, r & 7, c0 + b * kSub);
+                store_weights<kE, kR>(x, p_row, r & 7, b * kSub);
             }
             if (kCols > kSub) scores_read();
             if (key0 + 127 >= it.r.end) {
@@ -921,7 +939,7 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
                 // V's tile in the ring: K0, then K(j+1), V(j) in turn.
                 const uint32_t v_used = used + (j + 1 < it.m ? 2 * j + 2 : 2 * it.m - 1);
                 wait(&tl.full[v_used % S::kSlots], (v_used / S::kSlots) & 1);
-                if (key >= it.r.end && group == 0) {
+                if (key >= it.r.end) {
                     uint4* row = reinterpret_cast<uint4*>(ring + (v_used % S::kSlots) * S::kTile +
                                                           r * 128);
 #pragma unroll
@@ -953,12 +971,12 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) ptx::f2_unpack(l[i], sums[2 * i], sums[2 * i + 1]);
         const float mine = lane_sums<kCols>(sums, lane);
-        if (lane < kCols) tl.wmax[quarter][c0 + lane] = mine;
+        if (lane < kCols) tl.wmax[quarter][lane] = mine;
         group_sync(bar_id);
         const bool whole = c.j == 0 && it.m == it.r.n;
         const long long slot = static_cast<long long>(blockIdx.x) * 2 + (c.j == 0 ? 1 : 0);
         if (r < kCols) {
-            const int col = c0 + r;
+            const int col = r;
             const float sum = (tl.wmax[0][col] + tl.wmax[1][col]) +
                               (tl.wmax[2][col] + tl.wmax[3][col]);
             const int row = rows.row[col];
@@ -974,14 +992,14 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
                 p.part_ml[slot * kR + col] = make_float2(-rows.offset[col], sum);
             }
         }
-        wait(&tl.pv_done, (g - 1) & 1);
+        wait(&tl.pv_done[0], (g - 1) & 1);
         ptx::tc_fence_after();
         group_sync(bar_id);
 #pragma unroll
         for (int b = 0; b < kCols / 8; ++b) {
             float o[8];
             tmem_load(o_tm + b * 8, o);
-            if constexpr (S::kSideBySide) {
+            if constexpr (kE) {
                 float o1[8], o2[8];
                 tmem_load(o_tm + S::kN + b * 8, o1);
                 tmem_load(o_tm + 2 * S::kN + b * 8, o2);
@@ -990,7 +1008,7 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int col = c0 + b * 8 + i;
+                const int col = b * 8 + i;
                 if (whole) {
                     const int row = rows.row[col];
                     if (row >= 0)
@@ -1034,7 +1052,7 @@ __global__ void __launch_bounds__(Shape<kE, kR>::kThreads, Shape<kE, kR>::kCtasP
     const uint32_t sbase = ptx::smem_u32(smem);
     Tail& tl = *reinterpret_cast<Tail*>(smem + S::kOffTail);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kSoftWarps = S::kSoftThreads / 32;
+    constexpr int kSoftWarps = 4;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S::kSlots; ++i) {
@@ -1048,7 +1066,7 @@ __global__ void __launch_bounds__(Shape<kE, kR>::kThreads, Shape<kE, kR>::kCtasP
         }
         for (int i = 0; i < 4; ++i) ptx::mbar_init(ptx::smem_u32(&tl.scales_full[i]), 1);
         ptx::mbar_init(ptx::smem_u32(&tl.p_full), kSoftWarps);
-        ptx::mbar_init(ptx::smem_u32(&tl.pv_done), 1);
+        ptx::mbar_init(ptx::smem_u32(&tl.pv_done[0]), 1);
         ptx::mbar_init(ptx::smem_u32(&tl.drain), 1);
         tl.abort = 0;
         ptx::fence_mbar_init();
@@ -1072,11 +1090,11 @@ __global__ void __launch_bounds__(Shape<kE, kR>::kThreads, Shape<kE, kR>::kCtasP
 
     if (warp < kSoftWarps)
         softmax_role<kE, kR>(p, tl, smem + S::kOffQ, sbase + S::kOffP, smem + S::kOffRing, tmem,
-                             wc, warp >> 2);
+                             wc);
     else if (warp == kSoftWarps)
         mma_role<kE, kR>(p, tl, sbase + S::kOffQ, sbase + S::kOffP, sbase + S::kOffRing, tmem, wc);
     else
-        producer_role<kE, kR>(p, &tm_k, &tm_v, tl, sbase + S::kOffRing, wc, lane);
+        producer_role<S>(p, &tm_k, &tm_v, tl, sbase + S::kOffRing, wc, lane);
 
     ptx::tc_fence_before();
     __syncthreads();
@@ -1090,8 +1108,7 @@ __global__ void __launch_bounds__(Shape<kE, kR>::kThreads, Shape<kE, kR>::kCtasP
 // The parts of the items that a share's border cuts:
 //     O = sum_i 2^(u_i - U) acc_i / sum_i 2^(u_i - U) l_i,   U = max u_i.
 // Blocks (c, y): the item that begins in share c and goes on in the next ones.
-// With at most kMergeWarps parts a warp takes a row, rows 8 y .. 8 y + 7 to a
-// block; with more (long keys, few rows) a block takes rows y, y + 8, ... and a
+// With at most kMergeWarps parts a warp takes a row at a time; with more (long keys, few rows) a block takes rows y, y + 8, ... and a
 // warp every eighth part, and the warps' sums are joined in order.
 constexpr int kMergeWarps = 8;
 constexpr int kMergeParts = 8;  // parts whose loads are in flight together
@@ -1176,8 +1193,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     const float2* ml = p.part_ml + share;
     const float4* o = reinterpret_cast<const float4*>(p.part_o) + share * 32;
     if (parts <= kMergeWarps) {
-        const int c = blockIdx.y * kMergeWarps + warp;
-        if (there(c)) write(c, merge_parts(ml + c, o + c * 32, 0, 1, parts, kR, lane));
+        for (int c = blockIdx.y * kMergeWarps + warp; c < kR; c += gridDim.y * kMergeWarps)
+            if (there(c)) write(c, merge_parts(ml + c, o + c * 32, 0, 1, parts, kR, lane));
         return;
     }
     __shared__ float4 acc_s[kMergeWarps][32];

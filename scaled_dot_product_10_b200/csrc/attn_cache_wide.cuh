@@ -1,0 +1,517 @@
+// attn_cache_wide.cuh -- attention over a paged cache for more than 32 query
+// rows of a key/value head: drafted tokens of wide groups, chunks of prompts.
+//
+// Here the query rows lie on the 128 rows of the tensor core's tile:
+//     S [128 rows x 128 keys] = Q K^T      (A = Q tile,          B = K tile)
+//     O [128 rows x 128 dims] += P V       (A = P, Tensor Memory, B = V tile)
+// A thread owns a row, so the row's unit of weights, sum and limits are
+// registers, and the scales of the keys' pages are one factor for each run of
+// eight columns.  Two warps share 32 rows, each with half of the tile's keys.
+// The weights go to Tensor Memory, over the scores they came from, as the A
+// operand: kept in shared memory, the query rows' constants and P's pieces
+// beside the operands' reads filled its bandwidth (64 rows laid out as in
+// attn_cache_kernel.cuh took 2650 cycles a tile).
+//
+// The formulas, the pieces of Q and P, the schedule and the page loads are
+// those of attn_cache_kernel.cuh.
+#pragma once
+
+#include "attn_cache_kernel.cuh"
+
+namespace sdpa10 {
+namespace cache {
+
+template <bool kE_>
+struct WideShape {
+    static constexpr bool kE = kE_;
+    static constexpr int kRows = 128;
+    static constexpr int kSoftThreads = 256, kThreads = kSoftThreads + 64;
+    static constexpr int kQPieces = kE ? 2 : 1, kPPieces = kE ? 3 : 1;
+    static constexpr int kElem = kE ? 1 : 2;
+    static constexpr int kTile = 128 * kHeadDim * kElem;
+    static constexpr int kQPiece = kTile;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffRing = kQPieces * kQPiece;
+    static constexpr int kTail = 5120;
+    static constexpr int kCtasPerSm = 1;
+    static constexpr int kFit = (227 * 1024 - 1024 - kOffRing - kTail) / kTile;
+    static constexpr int kSlots = kFit < 8 ? kFit : 8;
+    static constexpr int kScaleTiles = 8;
+    static_assert(kSlots >= 3, "the ring needs K(j+1) beside K(j) and V(j)");
+    static constexpr int kOffTail = kOffRing + kSlots * kTile;
+    static constexpr int kAlloc = kOffTail + kTail + 1024;
+    // Tensor Memory: three tiles of scores (their weights in the same columns)
+    // and O.  With three, the scores of tile g go over the weights of tile
+    // g - 3, whose product is done by then.
+    static constexpr int kBufs = 3;
+    static constexpr uint32_t kTmemO = kBufs * 128;
+    static constexpr uint32_t kTmemCols = 512;
+};
+
+struct WideTail : Shared<8> {
+    float scale[2][128];  // of the rows' scores, this item's and the next one's
+    float half[2][128];   // maxima or sums of the two halves of a row's keys
+};
+static_assert(sizeof(WideTail) <= 5120, "");
+
+// kind::f8f6f4 with A in Tensor Memory: row m in lane m, 32 values along K in
+// eight 32-bit columns.
+__device__ __forceinline__ void mma_f8_ts_warp(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+
+__device__ __forceinline__ void tmem_store_bits(uint32_t t, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16};" ::"r"(t),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
+        : "memory");
+}
+
+// Barrier of the 256 softmax threads that also tells whether any says yes.
+__device__ __forceinline__ bool soft_any(bool yes) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.aligned.pred q, 1, 256, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(yes ? 1u : 0u)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void soft_sync() {
+    asm volatile("barrier.cta.sync.aligned 1, 256;" ::: "memory");
+}
+
+// ------------------------------------------------------------------ MMA
+template <bool kE>
+__device__ __forceinline__ void wide_mma_role(const FwdCacheParams& p, WideTail& tl, uint32_t sq,
+                                              uint32_t ring, uint32_t tmem, const WaitCtx& wc) {
+    using S = WideShape<kE>;
+    constexpr uint32_t kIdQK = kE ? idesc_e4m3_f32(128, 128, 0, 0) : idesc_bf16_f32(128, 128, 0, 0);
+    // P's pieces are E5M2 (code 1 in A's field).
+    constexpr uint32_t kIdPV =
+        kE ? idesc_e4m3_f32(128, 128, 0, 1) | (1u << 7) : idesc_bf16_f32(128, 128, 0, 1);
+    const uint32_t o_tm = tmem + S::kTmemO;
+    uint32_t used = 0, g = 0, pv = 0, items = 0;
+    bool ok = true;
+    auto wait_tile = [&]() -> bool {
+        return wait_bar_warp(ptx::smem_u32(&tl.full[used % S::kSlots]), (used / S::kSlots) & 1,
+                             wc);
+    };
+    auto qk = [&]() -> bool {
+        if (!wait_tile()) return false;
+        if (g >= 3) {
+            // Tile g - 3's product, or the last one issued to its barrier (the
+            // first scores of an item follow tile g - 1's): an older phase of
+            // the same parity cannot be told from the next.
+            const uint32_t d = pv == g ? g - 1 : g - 3;
+            if (!wait_bar_warp(ptx::smem_u32(&tl.pv_done[d & 1]), (d >> 1) & 1, wc)) return false;
+        }
+        ptx::tc_fence_after();
+        const uint32_t s_tm = tmem + (g % S::kBufs) * 128;
+        const uint32_t kb = desc_lo_sw128(ring + (used % S::kSlots) * S::kTile, 16);
+        const uint32_t qa = desc_lo_sw128(sq, 16);
+        if constexpr (kE) {
+#pragma unroll
+            for (int i = 0; i < S::kQPieces; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_f8_warp(s_tm, desc_from_lo(qa + ((i * S::kQPiece) >> 4) + 2 * k),
+                                desc_from_lo(kb + 2 * k), kIdQK, i + k > 0 ? 1u : 0u);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                ptx::mma_ss_warp(s_tm, desc_from_lo(qa + off), desc_from_lo(kb + off), kIdQK,
+                                 k > 0 ? 1u : 0u);
+            }
+        }
+        ptx::mma_commit_warp(ptx::smem_u32(&tl.s_full[g % S::kBufs]));
+        ptx::mma_commit_warp(ptx::smem_u32(&tl.empty[used % S::kSlots]));
+        ++used;
+        ++g;
+        return true;
+    };
+    auto weigh = [&](bool accumulate) -> bool {
+        if (!wait_tile()) return false;
+        if (!wait_bar_warp(ptx::smem_u32(&tl.p_full), pv & 1, wc)) return false;
+        ptx::tc_fence_after();
+        const uint32_t p_tm = tmem + (pv % S::kBufs) * 128;
+        const uint32_t vb =
+            desc_lo_sw128(ring + (used % S::kSlots) * S::kTile, kE ? S::kTile : 16384);
+        if constexpr (kE) {
+#pragma unroll
+            for (int i = 0; i < S::kPPieces; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_f8_ts_warp(o_tm, p_tm + i * 32 + k * 8,
+                                   desc_from_lo(vb + ((k * 4096) >> 4)), kIdPV,
+                                   accumulate || i + k > 0 ? 1u : 0u);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                ptx::mma_ts_warp(o_tm, p_tm + k * 8, desc_from_lo(vb + ((k * 2048) >> 4)), kIdPV,
+                                 accumulate || k > 0 ? 1u : 0u);
+        }
+        ptx::mma_commit_warp(ptx::smem_u32(&tl.pv_done[pv & 1]));
+        ptx::mma_commit_warp(ptx::smem_u32(&tl.empty[used % S::kSlots]));
+        ++used;
+        ++pv;
+        return true;
+    };
+    Cursor c = tl.cursor;
+    while (ok && c.left > 0) {
+        const Item it = cursor_item(p, c);
+        ok = wait_bar_warp(ptx::smem_u32(&tl.q_full), items & 1, wc);
+        ++items;
+        if (ok) ok = qk();
+        for (int i = 0; i < it.m && ok; ++i) {
+            if (i + 1 < it.m) ok = qk();
+            if (ok) ok = weigh(i > 0);
+        }
+        cursor_next(p, c, it);
+    }
+    ptx::mma_commit_warp(ptx::smem_u32(&tl.drain));
+    wait_slow(ptx::smem_u32(&tl.drain), 0, wc, false);
+    __syncwarp();
+}
+
+// ------------------------------------------------------------------ softmax
+// Eight warps: thread (row, side) has the row of its Tensor Memory lane and 64
+// of the tile's keys.  `dead` as in the narrow kernel.
+template <bool kE>
+__device__ __forceinline__ void wide_softmax_role(const FwdCacheParams& p, WideTail& tl,
+                                                  uint8_t* sq, uint8_t* ring, uint32_t tmem,
+                                                  const WaitCtx& wc) {
+    using S = WideShape<kE>;
+    const int tid = threadIdx.x, lane = tid & 31, side = tid >> 7;
+    const int row = tid & 127;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(row & ~31) << 16);
+    const uint32_t o_tm = lanes + S::kTmemO + side * 64;
+    const int box_log2 = 31 - __clz(p.box);
+    uint32_t g = 0, used = 0, items = 0;
+    bool dead = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!dead && !wait_bar_warp(ptx::smem_u32(bar), parity, wc)) dead = true;
+    };
+    auto stage = [&](const Item& it, int h) {
+        load_queries<kE, 128, 256>(p, tl.scale[items & 1], sq, kE ? S::kQPiece : 16384, it, h, tid);
+        ptx::fence_proxy_async_smem();
+        soft_sync();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&tl.q_full));
+    };
+
+    Cursor c = tl.cursor;
+    bool tail_part = false;
+    Item it;
+    if (c.left > 0) {
+        it = cursor_item(p, c);
+        stage(it, c.h);
+    }
+    while (c.left > 0) {
+        const RowView view = row_view(p, it, c.h, row);
+        const float q_scale = kE ? tl.scale[items & 1][row] : p.scale_log2;
+        const int shift = it.s.len - it.s.n;
+        const int min_last = p.causal ? min(it.s.kv - 1, shift + it.r.i0) : it.s.kv - 1;
+        const int max_first = p.window >= 0 ? shift + it.r.i1 - p.window : 0;
+        // Warps whose 32 rows are all past the item's last only keep step.
+        const bool active = (row & ~31) < (it.r.i1 - it.r.i0 + 1) * p.heads_per_tile;
+        float offset = kFresh, l = 0.f;
+
+        for (int j = 0; j < it.m; ++j, ++g) {
+            const int key0 = (it.r.tile0 + c.j + j) * 128;
+            const int first_key = key0 + side * 64;
+            const bool masked = key0 + 127 > min_last || key0 < max_first;
+            const uint32_t s_at = lanes + (g % S::kBufs) * 128;
+            if constexpr (kE) wait(&tl.scales_full[g & 7], (g >> 3) & 1);
+            const float4* scales = tl.scales[g & 7];
+            float x[64];
+            // x = S scale ks + log2(vs) + offset.
+            auto exponents = [&](float off) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    float s[32];
+                    tmem_load(s_at + side * 64 + b * 32, s);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float a = q_scale, o = off;
+                        if constexpr (kE) {
+                            const float4 sc = scales[(side * 64 + b * 32 + k * 8) >> box_log2];
+                            a *= sc.x;
+                            o += sc.y;
+                        }
+                        const uint64_t a2 = ptx::f2_pack(a, a), o2 = ptx::f2_pack(o, o);
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2) {
+                            const int at = b * 32 + k * 8 + i;
+                            ptx::f2_unpack(
+                                ptx::f2_fma(ptx::f2_pack(s[k * 8 + i], s[k * 8 + i + 1]), a2, o2),
+                                x[at], x[at + 1]);
+                        }
+                    }
+                }
+                if (masked) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        if (first_key + i > view.last || first_key + i < view.first)
+                            x[i] = -CUDART_INF_F;
+                }
+            };
+            auto largest = [&]() -> float {
+                float m[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    m[k] = x[16 * k];
+#pragma unroll
+                    for (int i = 1; i + 1 < 16; i += 2)
+                        m[k] = ptx::max3(m[k], x[16 * k + i], x[16 * k + i + 1]);
+                    m[k] = fmaxf(m[k], x[16 * k + 15]);
+                }
+                return ptx::max3(m[0], m[1], fmaxf(m[2], m[3]));
+            };
+
+            wait(&tl.s_full[g % S::kBufs], (g / S::kBufs) & 1);
+            ptx::tc_fence_after();
+            float top = -CUDART_INF_F;
+            if (active) {
+                exponents(offset);
+                top = largest();
+            }
+            // All of a row's scores have been read past this barrier.
+            ptx::tc_fence_before();
+            if (soft_any(top > kBias<kE> + kSlack<kE>)) {
+                if (active) {
+                    exponents(0.f);
+                    tl.half[side][row] = largest();
+                }
+                soft_sync();
+                if (active) {
+                    const float m = fmaxf(tl.half[0][row], tl.half[1][row]);
+                    const float old = offset;
+                    if (m > -CUDART_INF_F) offset = fminf(old, kBias<kE> - ceilf(m));
+                    const float alpha = ptx::ex2(offset - old);  // 0 for a row's first keys
+                    l *= alpha;
+                    if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                        wait(&tl.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+                        ptx::tc_fence_after();
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            float o[16];
+                            tmem_load(o_tm + b * 16, o);
+                            uint32_t u[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i] * alpha);
+                            tmem_store_bits(o_tm + b * 16, u);
+                        }
+                        ptx::tmem_wait_st();
+                    }
+                    exponents(offset);
+                }
+                ptx::tc_fence_before();
+                soft_sync();  // before the weights go over the scores
+            }
+            ptx::tc_fence_after();
+            if (active) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    float* w = x + 8 * k;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i] = ptx::ex2(w[i]);
+                    uint64_t s2 = ptx::f2_add(ptx::f2_pack(w[0], w[1]), ptx::f2_pack(w[2], w[3]));
+                    s2 = ptx::f2_add(s2, ptx::f2_add(ptx::f2_pack(w[4], w[5]),
+                                                     ptx::f2_pack(w[6], w[7])));
+                    float s0, s1;
+                    ptx::f2_unpack(s2, s0, s1);
+                    if constexpr (kE) {
+                        const float4 sc = scales[(side * 64 + k * 8) >> box_log2];
+                        l = fmaf(s0 + s1, sc.z, l);
+                        if (sc.w != 0.f) {  // V is zero there; its weights stay in l
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) w[i] = 0.f;
+                        }
+                    } else {
+                        l += s0 + s1;
+                    }
+                }
+                if constexpr (kE) {
+                    uint32_t piece[3][16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        split_weights(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3],
+                                      piece[0][i], piece[1][i], piece[2][i]);
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+                        tmem_store_bits(s_at + i * 32 + side * 16, piece[i]);
+                } else {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        uint32_t u[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            u[i] = ptx::pack_bf16x2(x[32 * b + 2 * i], x[32 * b + 2 * i + 1]);
+                        tmem_store_bits(s_at + side * 32 + b * 16, u);
+                    }
+                }
+                ptx::tmem_wait_st();
+            }
+            if (key0 + 127 >= it.r.end) {
+                // Slots past the end hold anything: zero them before 0 * NaN.
+                const uint32_t v_used = used + (j + 1 < it.m ? 2 * j + 2 : 2 * it.m - 1);
+                wait(&tl.full[v_used % S::kSlots], (v_used / S::kSlots) & 1);
+                if (key0 + row >= it.r.end && (!kE || side == 0)) {
+                    uint4* at = reinterpret_cast<uint4*>(ring + (v_used % S::kSlots) * S::kTile +
+                                                         side * 16384 + row * 128);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) at[i] = make_uint4(0, 0, 0, 0);
+                }
+                ptx::fence_proxy_async_smem();
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&tl.p_full));
+        }
+        used += 2 * it.m;
+
+        Cursor next = c;
+        cursor_next(p, next, it);
+        Item next_it = it;
+        ++items;
+        if (next.left > 0) {
+            next_it = cursor_item(p, next);
+            stage(next_it, next.h);
+        }
+
+        tl.half[side][row] = l;
+        soft_sync();
+        const float sum = tl.half[0][row] + tl.half[1][row];
+        const bool whole = c.j == 0 && it.m == it.r.n;
+        const long long slot = static_cast<long long>(blockIdx.x) * 2 + (c.j == 0 ? 1 : 0);
+        wait(&tl.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+        ptx::tc_fence_after();
+        if (active) {
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            if (side == 0) {
+                if (!whole) {
+                    p.part_ml[slot * 128 + row] = make_float2(-offset, sum);
+                } else if (view.row >= 0) {
+                    const int q = view.row / p.h_q;
+                    p.lse[static_cast<long long>(view.row - q * p.h_q) * p.total_q + q] =
+                        sum > 0.f ? (log2f(sum) - offset) * 0.69314718055994531f : -CUDART_INF_F;
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                float o[16];
+                tmem_load(o_tm + b * 16, o);
+                if (!whole) {
+                    float4* at = reinterpret_cast<float4*>(p.part_o + (slot * 128 + row) * kHeadDim +
+                                                           side * 64 + b * 16);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        at[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                } else if (view.row >= 0) {
+                    uint32_t u[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        u[i] = ptx::pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+                    uint4* at = reinterpret_cast<uint4*>(
+                        p.o + static_cast<long long>(view.row) * kHeadDim + side * 64 + b * 16);
+                    at[0] = make_uint4(u[0], u[1], u[2], u[3]);
+                    at[1] = make_uint4(u[4], u[5], u[6], u[7]);
+                }
+            }
+        }
+        ptx::tc_fence_before();
+        if (!whole && c.j == 0) {
+            tail_part = true;
+            if (tid == 0) {
+                const int head = c.h / p.head_tiles;
+                const int head0 = (c.h - head * p.head_tiles) * p.heads_per_tile;
+                const long long last = tl.begin + tl.chunk - it.m + it.r.n - 1;
+                p.meta[blockIdx.x] =
+                    make_int4(static_cast<int>(last / tl.chunk - blockIdx.x) + 1,
+                              it.s.row0 + it.r.i0, head * p.group + head0,
+                              (it.r.i1 - it.r.i0 + 1) |
+                                  (min(p.heads_per_tile, p.group - head0) << 16));
+            }
+        }
+        soft_sync();  // tl.half is free
+        c = next;
+        it = next_it;
+    }
+    if (tid == 0 && !tail_part && !p.whole) p.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+}
+
+template <bool kE>
+__global__ void __launch_bounds__(WideShape<kE>::kThreads, 1)
+    attn_fwd_cache_wide_kernel(const __grid_constant__ CUtensorMap tm_k,
+                               const __grid_constant__ CUtensorMap tm_v,
+                               const __grid_constant__ FwdCacheParams p) {
+    using S = WideShape<kE>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = ptx::smem_u32(smem);
+    WideTail& tl = *reinterpret_cast<WideTail*>(smem + S::kOffTail);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kSoftWarps = S::kSoftThreads / 32;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S::kSlots; ++i) {
+            ptx::mbar_init(ptx::smem_u32(&tl.full[i]), 1);
+            ptx::mbar_init(ptx::smem_u32(&tl.empty[i]), 1);
+        }
+        for (int i = 0; i < S::kScaleTiles; ++i)
+            ptx::mbar_init(ptx::smem_u32(&tl.scales_full[i]), 1);
+        ptx::mbar_init(ptx::smem_u32(&tl.q_full), kSoftWarps);
+        for (int i = 0; i < S::kBufs; ++i) ptx::mbar_init(ptx::smem_u32(&tl.s_full[i]), 1);
+        ptx::mbar_init(ptx::smem_u32(&tl.p_full), kSoftWarps);
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(ptx::smem_u32(&tl.pv_done[i]), 1);
+        ptx::mbar_init(ptx::smem_u32(&tl.drain), 1);
+        tl.abort = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&tm_k);
+        ptx::prefetch_tmap(&tm_v);
+    }
+    if (warp == kSoftWarps) {
+        ptx::tmem_alloc(ptx::smem_u32(&tl.tmem), S::kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = tl.tmem;
+    const WaitCtx wc{&tl.abort, p.status, p.timeout_ns};
+
+    grid_wait();
+    grid_launch_dependents();
+    find_share<S::kThreads>(p, tl);
+
+    if (warp < kSoftWarps)
+        wide_softmax_role<kE>(p, tl, smem + S::kOffQ, smem + S::kOffRing, tmem, wc);
+    else if (warp == kSoftWarps)
+        wide_mma_role<kE>(p, tl, sbase + S::kOffQ, sbase + S::kOffRing, tmem, wc);
+    else
+        producer_role<S>(p, &tm_k, &tm_v, tl, sbase + S::kOffRing, wc, lane);
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == kSoftWarps) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, S::kTmemCols);
+    }
+}
+
+}  // namespace cache
+}  // namespace sdpa10

@@ -166,6 +166,18 @@ def test_long_cache_is_split(kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,h_q", [(1, 1), (1, 12), (7, 4), (40, 1), (33, 5)])
+def test_shares_of_many_tiles_and_items(kind, n, h_q):
+    """Every CTA has several key tiles, most of them of more than one item."""
+    lens = [1400 + 97 * (i % 13) for i in range(90)]
+    if n * h_q > 100:
+        lens = lens[:30]
+    news = [max(1, n - i % 3) for i in range(len(lens))]
+    pool = Pool(lens, 48, 1, kind, seed=n)
+    run_attend(pool, lens, news, h_q, pad=2)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("scale", [0.0, -0.2, 1.5])
 def test_scales_of_the_scores(kind, scale):
     lens = [300, 40]
