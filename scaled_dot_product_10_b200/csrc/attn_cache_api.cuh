@@ -238,17 +238,16 @@ extern "C" int attn_cache_append(const attn_cache_t* c, const void* k, const voi
     const long long page_blocks =
         e4m3 ? static_cast<long long>(batch) * p.pages_per_seq * c->h_kv : 0;
     const int threads = e4m3 && most <= 8 ? 64 : (e4m3 && most <= 16 ? 128 : 256);
-    // Row role: one head for 8 lanes while that leaves SMs idle, more heads
-    // (whose angles are computed once) when there are rows enough.
+    // Row role: a warp takes 4 heads of a token while that leaves SMs idle, up
+    // to 16 when there are rows enough.
     p.heads_per_unit = 1;
-    while (p.heads_per_unit < 8 &&
-           static_cast<long long>(total) * p.row_heads / (2 * p.heads_per_unit) >= 148LL * 2048 / 8)
+    while (p.heads_per_unit < cache::kRowBatch && p.heads_per_unit * 4 < p.row_heads &&
+           static_cast<long long>(total) * p.row_heads / (8 * p.heads_per_unit) >= 148 * 48)
         p.heads_per_unit *= 2;
     const long long units =
-        p.row_heads == 0 ? 0
-                         : static_cast<long long>(total) *
-                               ((p.row_heads + p.heads_per_unit - 1) / p.heads_per_unit);
-    const long long row_blocks = (units * 8 + threads - 1) / threads;
+        static_cast<long long>(total) *
+        ((p.row_heads + 4 * p.heads_per_unit - 1) / (4 * p.heads_per_unit));
+    const long long row_blocks = (units * 32 + threads - 1) / threads;
     if (page_blocks + row_blocks > kMaxInt) return ATTN_ERR_INVALID;
     p.page_blocks = static_cast<int>(page_blocks);
     if (page_blocks + row_blocks == 0) return ATTN_OK;
@@ -258,10 +257,10 @@ extern "C" int attn_cache_append(const attn_cache_t* c, const void* k, const voi
     DeviceState* st = nullptr;
     rc = init_device(dev, &st);
     if (rc != ATTN_OK) return rc;
-    cache::attn_cache_append_kernel<<<static_cast<unsigned>(page_blocks + row_blocks),
-                                      static_cast<unsigned>(threads), 0,
-                                      static_cast<cudaStream_t>(stream)>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+    if (launch_after(cache::attn_cache_append_kernel,
+                     dim3(static_cast<unsigned>(page_blocks + row_blocks)), threads, 0,
+                     static_cast<cudaStream_t>(stream), p) != cudaSuccess)
+        return ATTN_ERR_CUDA;
     g_last_launches = 1;
     return ATTN_OK;
 }

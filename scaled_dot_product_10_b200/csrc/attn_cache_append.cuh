@@ -44,43 +44,61 @@ struct AppendParams {
     int page_blocks;      // CTAs of the page role (E4M3), before those of the row role
     int pages_per_seq;    // pages that max_seqlen rows can enter
     int row_heads;        // heads in the row role: h_q (E4M3) or h_q + 2 h_kv (BF16)
-    int heads_per_unit;   // of which one group of 8 lanes takes this many
+    int heads_per_unit;   // of which eight lanes take this many
 };
 
-// Eight lanes hold a row of 128 elements: two vectors of eight each, so that
-// the partner of every rotated element is in the same lane.
+// Eight lanes hold a row of 128 elements: two vectors of eight each, chosen so
+// that the partner of every rotated element is in the same lane and the lanes'
+// vectors are neighbours in memory.
 struct RowLane {
     int va, vb;  // the lane's two vectors (16 bytes of BF16 each)
-    int f0;      // first of its eight frequencies; -1: its elements pass
+    int fa, fb;  // first frequency of either vector's pairs (four interleaved
+                 // ones each, or eight shared by both); -1: its elements pass
 };
 
 __device__ __forceinline__ RowLane row_lane(int u, int rotary_dim, int interleaved) {
     RowLane r;
-    const int turned = rotary_dim >> 4;  // lanes that rotate
-    r.f0 = u < turned ? 8 * u : -1;
-    if (interleaved || u >= turned) {
-        r.va = 2 * u;
-        r.vb = 2 * u + 1;
+    r.va = u;
+    r.vb = u + 8;
+    if (interleaved) {
+        r.fa = 8 * r.va < rotary_dim ? 4 * r.va : -1;
+        r.fb = 8 * r.vb < rotary_dim ? 4 * r.vb : -1;
     } else {
-        r.va = u;
-        r.vb = u + turned;
+        const int turned = rotary_dim >> 4;  // lanes that rotate
+        if (u < turned) {
+            r.vb = u + turned;
+            r.fa = r.fb = 8 * u;
+        } else {
+            r.va = u + turned;
+            r.fa = r.fb = -1;
+        }
     }
     return r;
 }
 
+// Frequency of a lane's e-th pair, -1 if it passes.
+__device__ __forceinline__ int pair_frequency(const AppendParams& p, const RowLane& rl, int e) {
+    if (!p.interleaved) return rl.fa < 0 ? -1 : rl.fa + e;
+    return e < 4 ? (rl.fa < 0 ? -1 : rl.fa + e) : (rl.fb < 0 ? -1 : rl.fb + e - 4);
+}
+
+__device__ __forceinline__ void pair_angle(const AppendParams& p, int f, int pos, float& c,
+                                           float& s) {
+    c = 1.f;
+    s = 0.f;
+    if (f >= 0) {
+        constexpr double kInv2Pi = 0.15915494309189533577;
+        const double turns =
+            static_cast<double>(pos) * static_cast<double>(p.inv_freq[f]) * kInv2Pi;
+        sincospif(2.f * static_cast<float>(turns - rint(turns)), &s, &c);
+    }
+}
+
+// Cosines and sines of a lane's eight pairs at a position.
 __device__ __forceinline__ void row_angles(const AppendParams& p, const RowLane& rl, int pos,
                                            float (&c)[8], float (&s)[8]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        c[e] = 1.f;
-        s[e] = 0.f;
-        if (rl.f0 >= 0) {
-            constexpr double kInv2Pi = 0.15915494309189533577;
-            const double turns =
-                static_cast<double>(pos) * static_cast<double>(p.inv_freq[rl.f0 + e]) * kInv2Pi;
-            sincospif(2.f * static_cast<float>(turns - rint(turns)), &s[e], &c[e]);
-        }
-    }
+    for (int e = 0; e < 8; ++e) pair_angle(p, pair_frequency(p, rl, e), pos, c[e], s[e]);
 }
 
 __device__ __forceinline__ void unpack8(const uint4 w, float (&x)[8]) {
@@ -102,48 +120,48 @@ __device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], float inv) {
                       ptx::pack_e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
 }
 
-// Rotate a lane's two vectors in place.
+// Rotate a lane's two vectors in place (an element that passes has cosine 1
+// and sine 0, and keeps its bits).
 __device__ __forceinline__ void rotate(const RowLane& rl, int interleaved, const float (&c)[8],
                                        const float (&s)[8], float (&a)[8], float (&b)[8]) {
-    if (rl.f0 < 0) return;
     if (!interleaved) {
+        if (rl.fa < 0) return;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const float x = a[e], y = b[e];
             a[e] = x * c[e] - y * s[e];
             b[e] = y * c[e] + x * s[e];
         }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float x = a[2 * e], y = a[2 * e + 1];
-            a[2 * e] = x * c[e] - y * s[e];
-            a[2 * e + 1] = y * c[e] + x * s[e];
-            const float z = b[2 * e], w = b[2 * e + 1];
-            b[2 * e] = z * c[4 + e] - w * s[4 + e];
-            b[2 * e + 1] = w * c[4 + e] + z * s[4 + e];
-        }
+        return;
     }
+    auto turn = [](float& x, float& y, float co, float si) {
+        const float z = x;
+        x = z * co - y * si;
+        y = y * co + z * si;
+    };
+    if (rl.fa >= 0)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) turn(a[2 * e], a[2 * e + 1], c[e], s[e]);
+    if (rl.fb >= 0)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) turn(b[2 * e], b[2 * e + 1], c[4 + e], s[4 + e]);
 }
 
 // Largest |x| of a lane's elements, or |x| + |y| of its pairs where it rotates.
 __device__ __forceinline__ float row_bound(const RowLane& rl, int interleaved, const float (&a)[8],
                                            const float (&b)[8], bool pairs) {
     float m = 0.f;
+    if (pairs && !interleaved && rl.fa >= 0) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        float x = fabsf(a[e]), y = fabsf(b[e]);
-        if (pairs && rl.f0 >= 0) {
-            if (!interleaved) {
-                x += y;
-            } else if ((e & 1) == 0) {
-                x += fabsf(a[e + 1]);
-                y += fabsf(b[e + 1]);
-            } else {
-                x = y = 0.f;
-            }
-        }
-        m = fmaxf(m, fmaxf(x, y));
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(a[e]) + fabsf(b[e]));
+        return m;
+    }
+    const bool pa = pairs && interleaved && rl.fa >= 0, pb = pairs && interleaved && rl.fb >= 0;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        const float a0 = fabsf(a[e]), a1 = fabsf(a[e + 1]), b0 = fabsf(b[e]), b1 = fabsf(b[e + 1]);
+        m = fmaxf(m, pa ? a0 + a1 : fmaxf(a0, a1));
+        m = fmaxf(m, pb ? b0 + b1 : fmaxf(b0, b1));
     }
     return m;
 }
@@ -201,7 +219,11 @@ __device__ __forceinline__ SeqRows seq_rows(const AppendParams& p, int b) {
 // ------------------------------------------------------------------ pages
 // One CTA per (sequence, page that its new rows enter, head): the bounds of
 // the page's new rows, the scales, the older tokens if a scale grew, then the
-// rows themselves.  The rows are read twice, the second time from L2.
+// rows themselves, which are read a second time (from L2; keeping them as well
+// as the angles spilled).
+struct RowParts {
+    uint4 k0, k1, v0, v1;
+};
 __device__ __forceinline__ void append_page(const AppendParams& p, int block) {
     const int h = block % p.h_kv;
     const int bj = block / p.h_kv;
@@ -229,19 +251,29 @@ __device__ __forceinline__ void append_page(const AppendParams& p, int block) {
     const __nv_bfloat16* k = p.k + static_cast<long long>(row0) * p.k_stride + h * kHeadDim;
     const __nv_bfloat16* v = p.v + static_cast<long long>(row0) * p.v_stride + h * kHeadDim;
 
-    float kb = 0.f, vb = 0.f;
-    for (int r = slot; r < rows; r += slots) {
-        float a[8], c[8];
+    auto read = [&](int r) -> RowParts {
         const uint4* kr = reinterpret_cast<const uint4*>(k + r * p.k_stride);
         const uint4* vr = reinterpret_cast<const uint4*>(v + r * p.v_stride);
-        const uint4 k0 = kr[rl.va], k1 = kr[rl.vb], v0 = vr[rl.va], v1 = vr[rl.vb];
-        unpack8(k0, a);
-        unpack8(k1, c);
+        return RowParts{kr[rl.va], kr[rl.vb], vr[rl.va], vr[rl.vb]};
+    };
+    float kb = 0.f, vb = 0.f;
+    auto bound = [&](const RowParts& w) {
+        float a[8], c[8];
+        unpack8(w.k0, a);
+        unpack8(w.k1, c);
         kb = fmaxf(kb, row_bound(rl, p.interleaved, a, c, true));
-        unpack8(v0, a);
-        unpack8(v1, c);
+        unpack8(w.v0, a);
+        unpack8(w.v1, c);
         vb = fmaxf(vb, row_bound(rl, p.interleaved, a, c, false));
+    };
+    // The thread's first row, and its angles while that is under way.
+    float co[8], sn[8];
+    if (slot < rows) {
+        const RowParts w = read(slot);
+        row_angles(p, rl, static_cast<int>(lo) + slot, co, sn);
+        bound(w);
     }
+    for (int r = slot + slots; r < rows; r += slots) bound(read(r));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         kb = fmaxf(kb, __shfl_xor_sync(0xffffffffu, kb, o));
@@ -285,34 +317,39 @@ __device__ __forceinline__ void append_page(const AppendParams& p, int block) {
     if (v_old > 0.f && v_new > v_old) recode(p.v_pages, v_old * scale_inverse(v_new));
 
     const float k_inv = scale_inverse(k_new), v_inv = scale_inverse(v_new);
-    for (int r = slot; r < rows; r += slots) {
-        float a[8], c[8], co[8], sn[8];
-        const uint4* kr = reinterpret_cast<const uint4*>(k + r * p.k_stride);
-        const uint4* vr = reinterpret_cast<const uint4*>(v + r * p.v_stride);
-        const uint4 k0 = kr[rl.va], k1 = kr[rl.vb], v0 = vr[rl.va], v1 = vr[rl.vb];
-        row_angles(p, rl, static_cast<int>(lo) + r, co, sn);
+    auto write = [&](const RowParts& w, int r, const float (&cs)[8], const float (&si)[8]) {
+        float a[8], c[8];
         const long long at = base + (begin + r) * p.token_stride;
-        unpack8(k0, a);
-        unpack8(k1, c);
-        rotate(rl, p.interleaved, co, sn, a, c);
+        unpack8(w.k0, a);
+        unpack8(w.k1, c);
+        rotate(rl, p.interleaved, cs, si, a, c);
         reinterpret_cast<uint2*>(p.k_pages + at)[rl.va] = pack8_e4m3(a, k_inv);
         reinterpret_cast<uint2*>(p.k_pages + at)[rl.vb] = pack8_e4m3(c, k_inv);
-        unpack8(v0, a);
-        unpack8(v1, c);
+        unpack8(w.v0, a);
+        unpack8(w.v1, c);
         reinterpret_cast<uint2*>(p.v_pages + at)[rl.va] = pack8_e4m3(a, v_inv);
         reinterpret_cast<uint2*>(p.v_pages + at)[rl.vb] = pack8_e4m3(c, v_inv);
+    };
+    if (slot < rows) write(read(slot), slot, co, sn);
+    for (int r = slot + slots; r < rows; r += slots) {
+        const RowParts w = read(r);
+        row_angles(p, rl, static_cast<int>(lo) + r, co, sn);
+        write(w, r, co, sn);
     }
 }
 
 // ------------------------------------------------------------------ rows
-// Eight lanes take one token and heads_per_unit of its heads: queries, and for
-// BF16 pages keys and values.  The angles are computed once for all of them.
+// One warp per token and run of 4 heads_per_unit of its heads (queries, and for
+// BF16 pages keys and values): eight lanes to a head at a time.  The four
+// groups of lanes need the same angles: each computes two of a lane's eight
+// pairs and they are exchanged.
+constexpr int kRowBatch = 4;  // heads_per_unit at most, all read before any is written
 __device__ __forceinline__ void append_rows(const AppendParams& p, int block) {
-    const int groups = (p.row_heads + p.heads_per_unit - 1) / p.heads_per_unit;
-    const long long unit = static_cast<long long>(block) * (blockDim.x >> 3) + (threadIdx.x >> 3);
-    const long long tok = unit / groups;
+    const int runs = (p.row_heads + 4 * p.heads_per_unit - 1) / (4 * p.heads_per_unit);
+    const long long unit = static_cast<long long>(block) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const long long tok = unit / runs;
     if (tok >= p.total) return;
-    const int t = static_cast<int>(tok), g = static_cast<int>(unit % groups);
+    const int t = static_cast<int>(tok), run = static_cast<int>(unit % runs);
     int b;
     if (p.cu != nullptr) {
         int lo = 0, hi = p.batch;  // the last sequence that starts at or before t
@@ -328,51 +365,71 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int block) {
     const int i = t - s.row0;
     if (i < 0 || i >= min(s.n, p.max_seqlen)) return;  // padding
     const int pos = s.len - s.n + i;
-    const RowLane rl = row_lane(threadIdx.x & 7, p.rotary_dim, p.interleaved);
-    float co[8], sn[8];
-    row_angles(p, rl, pos, co, sn);
+    const int lane = threadIdx.x & 31, group = lane >> 3;
+    const RowLane rl = row_lane(lane & 7, p.rotary_dim, p.interleaved);
+    const int r0 = 4 * run * p.heads_per_unit + group;  // this group's heads: r0, r0 + 4, ...
+    const int r1 = min(p.row_heads, 4 * (run + 1) * p.heads_per_unit);
 
-    const int h1 = min(p.row_heads, (g + 1) * p.heads_per_unit);
+    uint4 w[kRowBatch][2];
+#pragma unroll
+    for (int j = 0; j < kRowBatch; ++j) {
+        const int r = r0 + 4 * j;
+        if (r >= r1) continue;
+        const __nv_bfloat16* src =
+            r < p.h_q ? p.q + t * p.q_stride + r * kHeadDim
+            : r < p.h_q + p.h_kv ? p.k + t * p.k_stride + (r - p.h_q) * kHeadDim
+                                 : p.v + t * p.v_stride + (r - p.h_q - p.h_kv) * kHeadDim;
+        w[j][0] = reinterpret_cast<const uint4*>(src)[rl.va];
+        w[j][1] = reinterpret_cast<const uint4*>(src)[rl.vb];
+    }
     // Where this token's keys and values go (BF16 pages).
     long long at = -1;
-    if (h1 > p.h_q && pos >= 0 && pos / p.page_size < p.max_pages) {
+    if (r1 > p.h_q && pos >= 0 && pos / p.page_size < p.max_pages) {
         const int pid = p.table[static_cast<long long>(b) * p.max_pages + pos / p.page_size];
         if (pid >= 0 && pid < p.num_pages)
             at = pid * p.page_stride + (pos % p.page_size) * p.token_stride;
     }
-#pragma unroll 4
-    for (int r = g * p.heads_per_unit; r < h1; ++r) {
-        const __nv_bfloat16* src;
-        __nv_bfloat16* dst;
-        bool turn = true;
-        if (r < p.h_q) {
-            src = p.q + t * p.q_stride + r * kHeadDim;
-            dst = p.q_out + (static_cast<long long>(t) * p.h_q + r) * kHeadDim;
-        } else {
-            if (at < 0) break;  // the remaining heads are keys and values
-            int h = r - p.h_q;
-            turn = h < p.h_kv;
-            if (!turn) h -= p.h_kv;
-            src = turn ? p.k + t * p.k_stride + h * kHeadDim : p.v + t * p.v_stride + h * kHeadDim;
-            dst = reinterpret_cast<__nv_bfloat16*>(turn ? p.k_pages : p.v_pages) + at +
-                  h * p.head_stride;
-        }
-        uint4 w0 = reinterpret_cast<const uint4*>(src)[rl.va];
-        uint4 w1 = reinterpret_cast<const uint4*>(src)[rl.vb];
-        if (turn && rl.f0 >= 0) {
+    float c2[2], s2[2], co[8], sn[8];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        pair_angle(p, pair_frequency(p, rl, 2 * group + e), pos, c2[e], s2[e]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        co[e] = __shfl_sync(0xffffffffu, c2[e & 1], (lane & 7) + 8 * (e >> 1));
+        sn[e] = __shfl_sync(0xffffffffu, s2[e & 1], (lane & 7) + 8 * (e >> 1));
+    }
+#pragma unroll
+    for (int j = 0; j < kRowBatch; ++j) {
+        const int r = r0 + 4 * j;
+        if (r >= r1) continue;
+        const bool is_q = r < p.h_q, is_v = r >= p.h_q + p.h_kv;
+        if (!is_q && at < 0) continue;
+        if (!is_v) {
             float a[8], c[8];
-            unpack8(w0, a);
-            unpack8(w1, c);
+            unpack8(w[j][0], a);
+            unpack8(w[j][1], c);
             rotate(rl, p.interleaved, co, sn, a, c);
-            w0 = pack8(a);
-            w1 = pack8(c);
+            w[j][0] = pack8(a);
+            w[j][1] = pack8(c);
         }
-        reinterpret_cast<uint4*>(dst)[rl.va] = w0;
-        reinterpret_cast<uint4*>(dst)[rl.vb] = w1;
+        const int h = r - p.h_q - (is_v ? p.h_kv : 0);
+        __nv_bfloat16* dst =
+            is_q ? p.q_out + (static_cast<long long>(t) * p.h_q + r) * kHeadDim
+                 : reinterpret_cast<__nv_bfloat16*>(is_v ? p.v_pages : p.k_pages) + at +
+                       h * p.head_stride;
+        reinterpret_cast<uint4*>(dst)[rl.va] = w[j][0];
+        reinterpret_cast<uint4*>(dst)[rl.vb] = w[j][1];
     }
 }
 
-__global__ void __launch_bounds__(256) attn_cache_append_kernel(const __grid_constant__ AppendParams p) {
+// Three CTAs of 256 threads on an SM: with fewer the loads in flight do not
+// cover the memory's latency, with four the rows spill (measured: 46.8 / 40.2 /
+// 43.6 us for 229 MB of ragged prompts with two, three, four).
+__global__ void __launch_bounds__(256, 3)
+    attn_cache_append_kernel(const __grid_constant__ AppendParams p) {
+    // All that came before on the stream is done and visible from here on.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (static_cast<int>(blockIdx.x) < p.page_blocks)
         append_page(p, blockIdx.x);
     else
