@@ -45,7 +45,7 @@ constexpr int kNarrowRows = 32;    // widest tile of this file's kernel
 // the unit is raised.  E4M3 pages: 2^11 p stays below 2^15 in FP16 and E5M2,
 // and the smallest E5M2 number is 2^-27 of the unit.
 template <bool kE> constexpr float kBias = kE ? 11.f : 0.f;
-template <bool kE> constexpr float kSlack = kE ? 4.f : 8.f;
+template <bool kE> constexpr float kSlack = kE ? 4.99f : 8.f;
 constexpr float kFresh = 1e30f;  // offset of a row that has seen no key
 
 struct FwdCacheParams {
@@ -186,37 +186,31 @@ __device__ __forceinline__ void mma_f8_warp(uint32_t d, uint64_t a, uint64_t b, 
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
 }
 
-// 32 lanes x 8, 16 or 32 consecutive columns.
+// 32 lanes x 8, 16 or 32 consecutive columns.  The wait is part of the same
+// asm, so nothing can use a value before it has come.
 __device__ __forceinline__ void tmem_load(uint32_t t, float (&r)[8]) {
-    uint32_t u[8];
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
-          "=r"(u[7])
-        : "r"(t));
-    ptx::tmem_wait_ld();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = __uint_as_float(u[i]);
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+        : "r"(t)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_load(uint32_t t, float (&r)[16]) {
-    uint32_t u[16];
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-        "%11, %12, %13, %14, %15}, [%16];"
-        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
-          "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]),
-          "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
-        : "r"(t));
-    ptx::tmem_wait_ld();
-#pragma unroll
-    for (int i = 0; i < 16; ++i) r[i] = __uint_as_float(u[i]);
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(t)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_load(uint32_t t, float (&r)[32]) {
-    uint32_t u[32];
-    ptx::tmem_ld32(t, u);
-    ptx::tmem_wait_ld();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) r[i] = __uint_as_float(u[i]);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(t)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_store(uint32_t t, const float (&r)[8]) {
     asm volatile(
@@ -316,7 +310,7 @@ struct Shared {
     float4 scales[kScaleTiles][16];
     uint64_t scales_full[kScaleTiles];
     uint64_t full[8], empty[8];
-    uint64_t q_full, s_full[3], s_free[2], p_full, pv_done[2], drain;
+    uint64_t q_full, s_full[3], s_free[2], p_full[3], pv_done[2], drain;
     long long begin;  // first unit of this share
     long long wsum[16];
     uint32_t tmem;
@@ -554,7 +548,7 @@ __device__ __forceinline__ void mma_role(const FwdCacheParams& p, Tail& tl, uint
     };
     auto weigh = [&](bool accumulate) -> bool {
         if (!wait_tile()) return false;
-        if (!wait_bar_warp(ptx::smem_u32(&tl.p_full), pv & 1, wc)) return false;
+        if (!wait_bar_warp(ptx::smem_u32(&tl.p_full[0]), pv & 1, wc)) return false;
         ptx::tc_fence_after();
         // Head dim (V) and query rows (P) lie along the 128-byte rows, keys
         // across them: 8 keys are 1 KiB.
@@ -952,7 +946,7 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
             ptx::fence_proxy_async_smem();
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&tl.p_full));
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&tl.p_full[0]));
         }
         used += 2 * it.m;
 
@@ -1065,7 +1059,7 @@ __global__ void __launch_bounds__(Shape<kE, kR>::kThreads, Shape<kE, kR>::kCtasP
             ptx::mbar_init(ptx::smem_u32(&tl.s_free[i]), kSoftWarps);
         }
         for (int i = 0; i < 4; ++i) ptx::mbar_init(ptx::smem_u32(&tl.scales_full[i]), 1);
-        ptx::mbar_init(ptx::smem_u32(&tl.p_full), kSoftWarps);
+        ptx::mbar_init(ptx::smem_u32(&tl.p_full[0]), kSoftWarps);
         ptx::mbar_init(ptx::smem_u32(&tl.pv_done[0]), 1);
         ptx::mbar_init(ptx::smem_u32(&tl.drain), 1);
         tl.abort = 0;

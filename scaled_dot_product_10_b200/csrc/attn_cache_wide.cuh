@@ -145,7 +145,7 @@ __device__ __forceinline__ void wide_mma_role(const FwdCacheParams& p, WideTail&
     };
     auto weigh = [&](bool accumulate) -> bool {
         if (!wait_tile()) return false;
-        if (!wait_bar_warp(ptx::smem_u32(&tl.p_full), pv & 1, wc)) return false;
+        if (!wait_bar_warp(ptx::smem_u32(&tl.p_full[pv & 1]), (pv >> 1) & 1, wc)) return false;
         ptx::tc_fence_after();
         const uint32_t p_tm = tmem + (pv % S::kBufs) * 128;
         const uint32_t vb =
@@ -379,7 +379,7 @@ __device__ __forceinline__ void wide_softmax_role(const FwdCacheParams& p, WideT
             }
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&tl.p_full));
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&tl.p_full[g & 1]));
         }
         used += 2 * it.m;
 
@@ -475,8 +475,12 @@ __global__ void __launch_bounds__(WideShape<kE>::kThreads, 1)
         for (int i = 0; i < S::kScaleTiles; ++i)
             ptx::mbar_init(ptx::smem_u32(&tl.scales_full[i]), 1);
         ptx::mbar_init(ptx::smem_u32(&tl.q_full), kSoftWarps);
-        for (int i = 0; i < S::kBufs; ++i) ptx::mbar_init(ptx::smem_u32(&tl.s_full[i]), 1);
-        ptx::mbar_init(ptx::smem_u32(&tl.p_full), kSoftWarps);
+        for (int i = 0; i < S::kBufs; ++i) {
+            ptx::mbar_init(ptx::smem_u32(&tl.s_full[i]), 1);
+        }
+        // Two: the warps may have weighed tile g + 1 before the issuer, waiting for
+        // V, has seen tile g's weights (tile g + 2's scores come after that).
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(ptx::smem_u32(&tl.p_full[i]), kSoftWarps);
         for (int i = 0; i < 2; ++i) ptx::mbar_init(ptx::smem_u32(&tl.pv_done[i]), 1);
         ptx::mbar_init(ptx::smem_u32(&tl.drain), 1);
         tl.abort = 0;
