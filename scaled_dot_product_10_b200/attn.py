@@ -163,7 +163,7 @@ def _check_out(t, name, shape, dtype, device):
     can check only null and alignment."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -558,16 +558,17 @@ def _cache_batch(page_table, seqlens_k, cu, cu_name, int32):
     return shape
 
 
-def _same_device(cache, stream, tensors):
+def _same_device(cache, stream, *tensors):
     """The cache's device, which every tensor of a call (and a torch stream)
     must share."""
     dev = cache.device
-    for name, t in tensors:
+    for t in tensors:
         if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
-    sdev = getattr(stream, "device", None)
-    if sdev is not None and sdev != dev:
-        raise ValueError(f"stream belongs to {sdev}, the cache to {dev}")
+            raise ValueError(f"a tensor of the call is on {t.device}, the cache on {dev}")
+    if stream is not None:
+        sdev = getattr(stream, "device", None)
+        if sdev is not None and sdev != dev:
+            raise ValueError(f"stream belongs to {sdev}, the cache to {dev}")
     return dev
 
 
@@ -611,9 +612,7 @@ def attn_cache_append(cache: KVCache, k, v, page_table, seqlens_k, cu_seqlens=No
         if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be a contiguous float32 vector")
         rotary_dim, freq_ptr = 2 * inv_freq.shape[0], inv_freq.data_ptr()
-    dev = _same_device(cache, stream, (("k", k), ("v", v), ("page_table", page_table),
-                                       ("seqlens_k", seqlens_k), ("cu_seqlens", cu_seqlens),
-                                       ("q", q), ("inv_freq", inv_freq)))
+    dev = _same_device(cache, stream, k, v, page_table, seqlens_k, cu_seqlens, q, inv_freq)
     with _on_device(dev):
         if q is not None:
             q_out = _out(q, q_out, "q_out", (total, h_q, 128), bf16, stream)
@@ -656,8 +655,7 @@ def attn_fwd_cache(q, cache: KVCache, page_table, seqlens_k, cu_seqlens_q=None,
     total_q, h_q, d = q.shape
     batch, max_pages = _cache_batch(page_table, seqlens_k, cu_seqlens_q, "cu_seqlens_q",
                                     torch.int32)
-    dev = _same_device(cache, stream, (("q", q), ("page_table", page_table),
-                                       ("seqlens_k", seqlens_k), ("cu_seqlens_q", cu_seqlens_q)))
+    dev = _same_device(cache, stream, q, page_table, seqlens_k, cu_seqlens_q)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if max_seqlen_q is None:

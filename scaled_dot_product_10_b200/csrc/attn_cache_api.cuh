@@ -103,6 +103,7 @@ int cache_rows(int group, int max_seqlen) {
 }
 
 constexpr int kWholeTiles = 4;  // see attn_fwd_cache
+constexpr int kNarrowItemUnits = 2, kWideItemUnits = 4;
 
 // The parts that a launch may leave: two for each CTA, of which the narrow
 // kernel has up to two on an SM.
@@ -319,6 +320,9 @@ extern "C" int attn_fwd_cache(const attn_cache_t* c, const void* q, void* o, flo
         c->h_kv * p.head_tiles;
     if (row_tiles > kMaxInt || row_tiles * key_tiles / 64 > kMaxInt) return ATTN_ERR_INVALID;
     p.whole = cap <= 128 * kWholeTiles;
+    // Measured: beginning and ending an item takes about as long as this many
+    // key tiles (see DESIGN's table for what evening that out gave).
+    p.item_units = rows > cache::kNarrowRows ? kWideItemUnits : kNarrowItemUnits;
 
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_ERR_CUDA;

@@ -67,6 +67,7 @@ struct FwdCacheParams {
     int head_tiles;      // row tiles across the group's heads
     int causal, window;  // window -1: none
     int whole;           // shares are of whole items: nothing to merge
+    int item_units;      // units of work that an item costs besides its key tiles
     float scale_log2;    // scale * log2(e)
     float* part_o;       // [ctas][2][R][128]
     float2* part_ml;     // [ctas][2][R]: log2 of the unit of weights, row sum in it
@@ -116,15 +117,16 @@ __device__ __forceinline__ RowTile row_tile(const FwdCacheParams& p, const Seq& 
     return r;
 }
 
-// Units of work of a row tile, of which a share has a run.
+// Units of work of an item, of which a share has a run: item_units for its
+// queries and its result, then one for each key tile.
 __device__ __forceinline__ int tile_units(const FwdCacheParams& p, const Seq& s, int t) {
-    return p.whole ? 1 : row_tile(p, s, t).n;
+    return p.whole ? 1 : p.item_units + row_tile(p, s, t).n;
 }
 
 __device__ __forceinline__ long long seq_units(const FwdCacheParams& p, const Seq& s) {
     if (p.whole) return s.tiles;
     long long u = 0;
-    for (int t = 0; t < s.tiles; ++t) u += row_tile(p, s, t).n;
+    for (int t = 0; t < s.tiles; ++t) u += tile_units(p, s, t);
     return u;
 }
 
@@ -149,7 +151,7 @@ __device__ __forceinline__ Item cursor_item(const FwdCacheParams& p, const Curso
 }
 
 __device__ __forceinline__ void cursor_next(const FwdCacheParams& p, Cursor& c, const Item& it) {
-    c.left -= p.whole ? 1 : it.m;
+    c.left -= p.whole ? 1 : it.m + p.item_units;
     c.j = 0;
     if (++c.t < it.s.tiles) return;
     c.t = 0;
@@ -356,9 +358,10 @@ __device__ __forceinline__ void find_share(const FwdCacheParams& p, T& tl) {
     const long long chunk = total >> 31 ? (total + grid - 1) / grid
                                         : (static_cast<uint32_t>(total) + gridDim.x - 1) / gridDim.x;
     const long long begin = chunk * blockIdx.x;
+    const long long rest = total - begin;
+    const int share = static_cast<int>(rest < 0 ? 0 : (rest < chunk ? rest : chunk));
     if (tid == 0) {
-        const long long rest = total - begin;
-        tl.cursor.left = static_cast<int>(rest < 0 ? 0 : (rest < chunk ? rest : chunk));
+        if (begin >= total) tl.cursor.left = 0;
         tl.chunk = static_cast<int>(chunk);
         tl.begin = begin;
     }
@@ -392,7 +395,13 @@ __device__ __forceinline__ void find_share(const FwdCacheParams& p, T& tl) {
                 }
                 tl.cursor.b = b;
                 tl.cursor.t = t;
-                tl.cursor.j = left;
+                tl.cursor.j = 0;
+                tl.cursor.left = share;
+                if (!p.whole) {
+                    // Within the item's own units: its first tile, the rest of them paid.
+                    tl.cursor.j = max(left - p.item_units, 0);
+                    tl.cursor.left = share - max(p.item_units - left, 0);
+                }
             }
             if (p.batch > kThreads && run > begin) break;  // the same for every thread
         }

@@ -25,7 +25,10 @@ template <bool kE_>
 struct WideShape {
     static constexpr bool kE = kE_;
     static constexpr int kRows = 128;
-    static constexpr int kSoftThreads = 256, kThreads = kSoftThreads + 64;
+    // Two softmax warpgroups and one of the MMA issuer, the producer and two idle
+    // warps, whose registers go to the other two: 2 * 128 * 216 + 128 * 72 = 384 * 168.
+    static constexpr int kSoftThreads = 256, kThreads = kSoftThreads + 128;
+    static constexpr int kRegsSoft = 216, kRegsOther = 72;
     static constexpr int kQPieces = kE ? 2 : 1, kPPieces = kE ? 3 : 1;
     static constexpr int kElem = kE ? 1 : 2;
     static constexpr int kTile = 128 * kHeadDim * kElem;
@@ -502,12 +505,16 @@ __global__ void __launch_bounds__(WideShape<kE>::kThreads, 1)
     grid_launch_dependents();
     find_share<S::kThreads>(p, tl);
 
-    if (warp < kSoftWarps)
+    if (warp < kSoftWarps) {
+        ptx::reg_alloc<S::kRegsSoft>();
         wide_softmax_role<kE>(p, tl, smem + S::kOffQ, smem + S::kOffRing, tmem, wc);
-    else if (warp == kSoftWarps)
-        wide_mma_role<kE>(p, tl, sbase + S::kOffQ, sbase + S::kOffRing, tmem, wc);
-    else
-        producer_role<S>(p, &tm_k, &tm_v, tl, sbase + S::kOffRing, wc, lane);
+    } else {
+        ptx::reg_dealloc<S::kRegsOther>();
+        if (warp == kSoftWarps)
+            wide_mma_role<kE>(p, tl, sbase + S::kOffQ, sbase + S::kOffRing, tmem, wc);
+        else if (warp == kSoftWarps + 1)
+            producer_role<S>(p, &tm_k, &tm_v, tl, sbase + S::kOffRing, wc, lane);
+    }
 
     ptx::tc_fence_before();
     __syncthreads();
