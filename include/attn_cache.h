@@ -88,7 +88,7 @@ typedef struct {
  *                Rows from cu_seqlens[batch] on are padding: not read, and
  *                q_out is left as it was there
  *   max_seqlen   upper bound of the sequences' new rows; rows past it are
- *                not processed
+ *                not processed (positions stay those of the whole sequence)
  *   inv_freq     device, fp32 [rotary_dim / 2] (null iff rotary_dim is 0)
  *   rotary_dim   0 .. 128, a multiple of 16: the first rotary_dim elements of
  *                a head are rotated, the others pass unchanged
@@ -156,11 +156,13 @@ int attn_cache_append(const attn_cache_t* cache, const void* k, const void* v, c
  * Numerics: BF16 pages as attn_fwd (P rounded to BF16).  E4M3 pages go to the
  * tensor core as they are; a query is the sum of two E4M3 numbers (exact for
  * elements within 2^-9 of its largest, the others within 2^-18 of that) and a
- * weight P the sum of three E5M2 numbers (9 bits, from the largest down to
- * 2^-23 of it), so neither loses what BF16 operands would keep.  Sums are
- * FP32.
+ * weight P, rounded to FP16, the sum of three E5M2 numbers (9 bits from the
+ * largest down to 2^-18 of it, and no less than 2^-27 of it apart), so neither
+ * loses what BF16 operands would keep.  Sums are FP32.  The same call gives the
+ * same bits each time.
  *
- * Two launches.  Errors as attn_cache_append, plus ATTN_ERR_INVALID for a
+ * Two launches, or one where the rows of page_table hold at most 512 keys
+ * (attn_last_launch_count tells).  Errors as attn_cache_append, plus ATTN_ERR_INVALID for a
  * non-finite scale, a window without causal and a workspace too small.
  */
 int attn_fwd_cache(const attn_cache_t* cache, const void* q, void* o, float* lse,

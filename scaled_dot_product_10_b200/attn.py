@@ -648,7 +648,9 @@ def attn_fwd_cache(q, cache: KVCache, page_table, seqlens_k, cu_seqlens_q=None,
     gets 0 and -inf, rows behind the last sequence are left as they were.
 
     ``workspace``: a CUDA uint8 tensor of at least
-    :func:`cache_workspace_bytes` bytes, allocated here if None.  Two launches.
+    :func:`cache_workspace_bytes` bytes, allocated here if None; calls that may
+    run at the same time need one each.  Two launches, or one where the rows of
+    ``page_table`` hold at most 512 keys.
     """
     import torch
     q_stride = _packed_rows("q", q, None, torch.bfloat16)

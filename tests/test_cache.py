@@ -130,7 +130,7 @@ def test_several_rows(kind, news, causal):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
-@pytest.mark.parametrize("window", [0, 1, 100, 127, 128, 300, 5000])
+@pytest.mark.parametrize("window", [0, 1, 100, 127, 128, 300, 5000, 2 ** 31 - 1])
 def test_windows(kind, window):
     lens, news = [700, 130, 60], [1, 130, 7]
     pool = Pool(lens, 32, 2, kind, seed=window)
@@ -277,6 +277,51 @@ def test_strided_queries_stream_and_graph():
     assert attn.attn_status() == attn.ATTN_OK
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_two_streams_at_once(kind):
+    """Calls side by side, each with a workspace of its own."""
+    lens = [3000, 700]
+    pool = Pool(lens, 64, 1, kind, seed=14)
+    seqlens = torch.tensor(lens, dtype=torch.int32).cuda()
+    news = [1, 40]
+    streams = [torch.cuda.Stream() for _ in news]
+    cases = []
+    for n in news:
+        q = torch.randn(2 * n, 4, 128, generator=torch.Generator().manual_seed(n)).to(torch.bfloat16)
+        want = ref.attend(q, *pool.pages, *pool.scale, pool.table, lens, [n, n], True, -1, 128 ** -0.5)
+        cases.append((q.cuda(), want))
+    torch.cuda.synchronize()
+    for _ in range(4):
+        outs = [attn.attn_fwd_cache(q, pool.cache, pool.d_table, seqlens, stream=s)
+                for (q, _), s in zip(cases, streams)]
+        torch.cuda.synchronize()
+        for (o, lse), (_, want) in zip(outs, cases):
+            ref.assert_attend(o, lse, want)
+    assert attn.attn_status() == attn.ATTN_OK
+
+
+def test_launches_and_bounds():
+    """One launch for short tables; rows past max_seqlen_q are left alone."""
+    pool = Pool([500, 512], 16, 2, "e4m3", seed=15)
+    run_attend(pool, [500, 512], [1, 1], 8)
+    assert attn.last_launch_count() == 1
+    pool = Pool([500, 513], 16, 2, "e4m3", seed=15)
+    run_attend(pool, [500, 513], [1, 1], 8)
+    assert attn.last_launch_count() == 2
+    q = torch.randn(8, 4, 128).to(torch.bfloat16).cuda()
+    sl = torch.tensor([500, 513], dtype=torch.int32).cuda()
+    o = torch.full((8, 4, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((4, 8), 7.0, device="cuda")
+    attn.attn_fwd_cache(q, pool.cache, pool.d_table, sl, max_seqlen_q=3, o=o, lse=lse)
+    whole, _ = attn.attn_fwd_cache(q, pool.cache, pool.d_table, sl)
+    assert attn.attn_status() == attn.ATTN_OK
+    for i in range(8):
+        if i % 4 == 3:
+            assert bool((o[i] == 7).all()) and bool((lse[:, i] == 7).all())
+        else:
+            assert float((o[i].float() - whole[i].float()).abs().max()) < 2.0 ** -5
+
+
 # ------------------------------------------------------------------ append
 def inv_freq_of(rotary):
     if rotary == 0:
@@ -415,6 +460,60 @@ def test_append_refuses_bad_places(kind):
     run_append(pool, [3], [10], 2)     # seven rows before the start
     pool = Pool([40], 8, 1, kind, seed=9, filled=[30])
     run_append(pool, [60], [30], 2)    # twenty past the table
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_append_captured_and_on_a_stream(kind):
+    """A captured step appends wherever its tensors point when it is replayed."""
+    lens, page = [20, 5], 8
+    pool = Pool([40, 40], page, 2, kind, seed=12, filled=[19, 4])
+    g = torch.Generator().manual_seed(3)
+    inv = inv_freq_of(64)
+    k, v = (torch.randn(2, 2, 128, generator=g).to(torch.bfloat16) for _ in range(2))
+    dk, dv, dinv = k.cuda(), v.cuda(), inv.cuda()
+    seqlens = torch.tensor(lens, dtype=torch.int32).cuda()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        attn.attn_cache_append(pool.cache, dk, dv, pool.d_table, seqlens, inv_freq=dinv)
+    side = torch.cuda.Stream()
+    for step in range(12):
+        before = [x.cpu().clone() for x in pool.d_pages]
+        want = ref.append(k, v, *before, *[None if s is None else s.cpu() for s in pool.d_scale],
+                          pool.table, lens, [1, 1], inv, False)
+        if step % 2:
+            graph.replay()
+        else:
+            side.wait_stream(torch.cuda.current_stream())
+            attn.attn_cache_append(pool.cache, dk, dv, pool.d_table, seqlens, inv_freq=dinv,
+                                   stream=side)
+            torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        for t in range(2):
+            ref.assert_pages(pool.d_pages[t], want[t], kind == "e4m3", want[4], before[t])
+            if kind == "e4m3":
+                assert torch.equal(pool.d_scale[t].cpu().double(), want[2 + t])
+        lens = [n + 1 for n in lens]
+        k = k * (1.5 if step % 3 else 0.2)
+        dk.copy_(k)
+        seqlens.copy_(torch.tensor(lens, dtype=torch.int32))
+
+
+def test_append_rows_past_the_bound():
+    """max_seqlen cuts a sequence's rows; the others keep their positions."""
+    for kind in ("bf16", "e4m3"):
+        pool = Pool([30], 8, 1, kind, seed=13, filled=[20])
+        x = torch.randn(10, 2, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+        before = [p.cpu().clone() for p in pool.d_pages]
+        d = x.cuda()
+        attn.attn_cache_append(pool.cache, d[:, :1], d[:, 1:], pool.d_table,
+                               torch.tensor([30], dtype=torch.int32).cuda(), max_seqlen=6,
+                               inv_freq=inv_freq_of(128).cuda())
+        # the first six rows, at positions 20 .. 25
+        want = ref.append(x[:6, :1], x[:6, 1:], *before,
+                          *[None if s is None else s.clone() for s in pool.scale], pool.table,
+                          [26], [6], inv_freq_of(128), False)
+        for t in range(2):
+            ref.assert_pages(pool.d_pages[t], want[t], kind == "e4m3", want[4], before[t])
 
 
 def test_offsets_past_32_bits():

@@ -1,0 +1,246 @@
+"""CPU model of the hand-overs inside the paged-cache attention kernels.
+
+The producer, the MMA issuer and the softmax warps run as coroutines in random
+order over random items; barriers have phases that a waiter can only tell apart
+by one parity bit, copies and products finish late (products in order).  Every
+buffer carries the tile it holds, so a read of the wrong tile, a write over one
+still in use and a wait that never ends are all seen.  The rule that hid a
+phase on the GPU (one barrier for the weights of the wide kernel) is kept as a
+planted mistake.
+"""
+from __future__ import annotations
+
+import random
+
+import pytest
+
+
+class Barrier:
+    def __init__(self, count):
+        self.count, self.left, self.phase = count, count, 0
+
+    def arrive(self):
+        self.left -= 1
+        if self.left == 0:
+            self.phase, self.left = self.phase + 1, self.count
+
+    def passed(self, parity):
+        return (self.phase & 1) != parity
+
+
+class Model:
+    """kind: "narrow" or "wide"; warps: softmax warps of a tile."""
+
+    def __init__(self, rng, kind, items, slots, warps, p_bars):
+        self.rng, self.kind, self.items, self.slots, self.warps = rng, kind, items, slots, warps
+        self.p_bars = p_bars
+        self.bufs = 3 if kind == "wide" else 2
+        self.full = [Barrier(1) for _ in range(slots)]
+        self.empty = [Barrier(1) for _ in range(slots)]
+        self.q_full = Barrier(warps)
+        self.s_full = [Barrier(1) for _ in range(self.bufs)]
+        self.s_free = [Barrier(warps) for _ in range(2)]
+        self.p_full = [Barrier(warps) for _ in range(p_bars)]
+        self.n_done = 2 if kind == "wide" else 1
+        self.pv_done = [Barrier(1) for _ in range(self.n_done)]
+        self.ring = [None] * slots      # what a slot holds; ("K" | "V", tile)
+        self.s_buf = [None] * self.bufs  # tile whose scores (wide: or weights) are there
+        self.p_tile = [dict() for _ in range(self.bufs if kind == "wide" else 1)]  # warp -> tile
+        self.q_item = [None] * warps
+        self.queue = []                 # tensor-core work, in order
+        self.loads = []                 # copies under way
+        self.group = [0, 0]             # the softmax warps' own barrier: arrived, generation
+        self.weighed = []
+
+    # -------------------------------------------------------------- roles
+    def producer(self):
+        n = 0
+        tile = 0
+        for m in self.items:
+            order = [("K", 0)]
+            for j in range(m):
+                if j + 1 < m:
+                    order.append(("K", j + 1))
+                order.append(("V", j))
+            for what, j in order:
+                slot = n % self.slots
+                while not self.empty[slot].passed(((n // self.slots) & 1) ^ 1):
+                    yield
+                self.loads.append((slot, (what, tile + j)))
+                n += 1
+                yield
+            tile += m
+
+    def done(self, tile):
+        """The barrier and parity of a tile's product."""
+        return (self.pv_done[tile & 1], (tile >> 1) & 1) if self.kind == "wide" \
+            else (self.pv_done[0], tile & 1)
+
+    def issuer(self):
+        used = g = pv = 0
+        for item, m in enumerate(self.items):
+            while not self.q_full.passed(item & 1):
+                yield
+
+            def scores():
+                nonlocal used, g
+                slot = used % self.slots
+                while not self.full[slot].passed((used // self.slots) & 1):
+                    yield
+                if self.kind == "wide":
+                    if g >= 3:
+                        d = g - 1 if pv == g else g - 3
+                        bar, parity = self.done(d)
+                        while not bar.passed(parity):
+                            yield
+                elif g >= 2:
+                    while not self.s_free[g & 1].passed(((g >> 1) - 1) & 1):
+                        yield
+                assert self.ring[slot] == ("K", g)
+                assert all(q == item for q in self.q_item), "queries not there"
+                self.queue.append(("S", g, slot))
+                used, g = used + 1, g + 1
+
+            def weigh():
+                nonlocal used, pv
+                slot = used % self.slots
+                while not self.full[slot].passed((used // self.slots) & 1):
+                    yield
+                k = len(self.p_full)
+                while not self.p_full[pv % k].passed((pv // k) & 1):
+                    yield
+                assert self.ring[slot] == ("V", pv)
+                self.queue.append(("O", pv, slot))
+                used, pv = used + 1, pv + 1
+
+            yield from scores()
+            for j in range(m):
+                if j + 1 < m:
+                    yield from scores()
+                yield from weigh()
+
+    def softmax(self, warp):
+        g = 0
+        self.q_item[warp] = 0
+        self.q_full.arrive()
+        yield
+        for item, m in enumerate(self.items):
+            for j in range(m):
+                b = g % self.bufs
+                while not self.s_full[b].passed((g // self.bufs) & 1):
+                    yield
+                assert self.s_buf[b] == g, "scores of another tile"
+                # the warps' barrier with its vote: all have read their scores
+                generation = self.group[1]
+                self.group[0] += 1
+                if self.group[0] == self.warps:
+                    self.group = [0, generation + 1]
+                while self.group[1] == generation:
+                    yield
+                if self.kind == "narrow":
+                    self.s_free[g & 1].arrive()
+                    yield
+                    if g > 0:
+                        bar, parity = self.done(g - 1)
+                        while not bar.passed(parity):
+                            yield
+                    self.p_tile[0][warp] = g
+                else:
+                    self.p_tile[b][warp] = g
+                yield
+                self.p_full[g % len(self.p_full)].arrive()
+                g += 1
+                yield
+            if item + 1 < len(self.items):
+                self.q_item[warp] = item + 1
+                # no warp goes on before all have staged their rows
+                generation = self.group[1]
+                self.group[0] += 1
+                if self.group[0] == self.warps:
+                    self.group = [0, generation + 1]
+                while self.group[1] == generation:
+                    yield
+                self.q_full.arrive()
+            bar, parity = self.done(g - 1)
+            while not bar.passed(parity):
+                yield
+
+    # -------------------------------------------------------------- hardware
+    def hardware(self):
+        """A copy or the oldest product finishes."""
+        if self.loads and (not self.queue or self.rng.random() < 0.5):
+            slot, what = self.loads.pop(self.rng.randrange(len(self.loads)))
+            self.ring[slot] = what
+            self.full[slot].arrive()
+        elif self.queue:
+            what, tile, slot = self.queue.pop(0)
+            if what == "S":
+                b = tile % self.bufs
+                if self.kind == "wide" and tile >= 3:
+                    assert tile - 3 in self.weighed, "scores over weights still to be used"
+                assert self.ring[slot] == ("K", tile)
+                self.s_buf[b] = tile
+                self.s_full[b].arrive()
+            else:
+                p = self.p_tile[tile % self.bufs if self.kind == "wide" else 0]
+                assert len(p) == self.warps and set(p.values()) == {tile}, "weights of another tile"
+                assert self.ring[slot] == ("V", tile)
+                self.weighed.append(tile)
+                (self.pv_done[tile & 1] if self.kind == "wide" else self.pv_done[0]).arrive()
+            self.empty[slot].arrive()
+        else:
+            return False
+        return True
+
+    def run(self):
+        roles = [self.producer(), self.issuer()] + [self.softmax(w) for w in range(self.warps)]
+        weights = [self.rng.choice([1, 1, 8]) for _ in roles] + [self.rng.choice([1, 4, 16])]
+        alive = list(range(len(roles)))
+        idle = 0
+        while alive:
+            i = self.rng.choices(range(len(weights)), weights)[0]
+            before = (len(self.queue), len(self.loads), self.state())
+            if i == len(roles):
+                self.hardware()
+            elif i in alive:
+                try:
+                    next(roles[i])
+                except StopIteration:
+                    alive.remove(i)
+            idle = 0 if (len(self.queue), len(self.loads), self.state()) != before else idle + 1
+            assert idle < 4000, "a wait that nothing ends"
+        while self.hardware():
+            pass
+        assert self.weighed == list(range(sum(self.items)))
+
+    def state(self):
+        bars = (self.full + self.empty + self.s_full + self.s_free + self.p_full + self.pv_done +
+                [self.q_full])
+        return tuple((b.phase, b.left) for b in bars) + tuple(self.group)
+
+
+def items_of(rng):
+    return [rng.choice([1, 1, 2, 3, 5, 9]) for _ in range(rng.randint(1, 6))]
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_narrow(seed):
+    rng = random.Random(seed)
+    Model(rng, "narrow", items_of(rng), rng.choice([3, 5, 6]), 4, 1).run()
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_wide(seed):
+    rng = random.Random(1000 + seed)
+    Model(rng, "wide", items_of(rng), rng.choice([5, 8]), 3, 2).run()
+
+
+def test_one_barrier_for_wide_weights_is_caught():
+    caught = 0
+    for seed in range(60):
+        rng = random.Random(2000 + seed)
+        try:
+            Model(rng, "wide", items_of(rng), rng.choice([5, 8]), 3, 1).run()
+        except AssertionError as e:
+            caught += "nothing ends" in str(e) or "another tile" in str(e)
+    assert caught > 0
