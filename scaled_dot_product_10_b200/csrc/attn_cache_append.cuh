@@ -11,6 +11,13 @@
 // rotation of it exceeds: the scale depends on the BF16 inputs alone.  A power
 // of two costs a floating-point format no precision, and coding a page again
 // under a larger one only shifts exponents.
+//
+// Bound: the memory, and beside it for E4M3 pages the arithmetic (the issue
+// slots are 64 % full).  BF16, eight prompts of up to 2048 tokens, 16 heads:
+// 229 MB in 38.2 us, 6.0 TB/s.  E4M3, 32768 tokens, two heads, and their
+// queries: 319 MB in 55.9 us, 5.7 TB/s.  One token: 4.1 us, a launch and its
+// chain of dependent reads (length, page, scale, row).  A plain copy moves
+// 6.55 TB/s.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -22,6 +29,17 @@
 
 namespace sdpa10 {
 namespace cache {
+
+// Threads of a CTA, as measured with the registers of twelve CTAs of 64 (us):
+//      threads               32     64     96    128    256
+//      32768 tokens        64.8   58.7   59.3   58.9   61.0
+//      64 times 5 tokens    8.7    7.0    8.2    8.7   13.5
+// (few threads for a page spread a short step over the SMs), and with 64
+// threads, registers for
+//      CTAs on an SM         10     12     14     16     18
+//      32768 tokens        61.5   58.6   55.9   62.6   72.4
+// (loads in flight against spilt registers; 14 spill 56 bytes).
+constexpr int kAppendThreads = 64, kAppendCtasPerSm = 14;
 
 struct AppendParams {
     const __nv_bfloat16* q;
@@ -244,7 +262,8 @@ __device__ __forceinline__ void append_page(const AppendParams& p, int block) {
     const int pid = p.table[static_cast<long long>(b) * p.max_pages + page];
     if (pid < 0 || pid >= p.num_pages) return;
 
-    const int slots = blockDim.x >> 3, slot = threadIdx.x >> 3;
+    constexpr int slots = kAppendThreads >> 3;
+    const int slot = threadIdx.x >> 3;
     const RowLane rl = row_lane(threadIdx.x & 7, p.rotary_dim, p.interleaved);
     const int rows = static_cast<int>(hi - lo), begin = static_cast<int>(lo - page0);
     const int row0 = s.row0 + static_cast<int>(lo - first);
@@ -279,7 +298,7 @@ __device__ __forceinline__ void append_page(const AppendParams& p, int block) {
         kb = fmaxf(kb, __shfl_xor_sync(0xffffffffu, kb, o));
         vb = fmaxf(vb, __shfl_xor_sync(0xffffffffu, vb, o));
     }
-    __shared__ float red[2][8];
+    __shared__ float red[2][kAppendThreads / 32];
     if ((threadIdx.x & 31) == 0) {
         red[0][threadIdx.x >> 5] = kb;
         red[1][threadIdx.x >> 5] = vb;
@@ -288,7 +307,8 @@ __device__ __forceinline__ void append_page(const AppendParams& p, int block) {
     const float k_old = begin > 0 ? p.k_scale[si] : 0.f;
     const float v_old = begin > 0 ? p.v_scale[si] : 0.f;
     __syncthreads();
-    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
+#pragma unroll
+    for (int w = 0; w < kAppendThreads / 32; ++w) {
         kb = fmaxf(kb, red[0][w]);
         vb = fmaxf(vb, red[1][w]);
     }
@@ -300,7 +320,7 @@ __device__ __forceinline__ void append_page(const AppendParams& p, int block) {
     const long long base = pid * p.page_stride + h * p.head_stride;
     // Older tokens under a scale that grew: 16 codes at a time.
     auto recode = [&](uint8_t* pages, float factor) {
-        for (int i = threadIdx.x; i < begin * 8; i += blockDim.x) {
+        for (int i = threadIdx.x; i < begin * 8; i += kAppendThreads) {
             uint4* at = reinterpret_cast<uint4*>(pages + base + (i >> 3) * p.token_stride) + (i & 7);
             uint4 w = *at;
             uint32_t* c = reinterpret_cast<uint32_t*>(&w);
@@ -346,7 +366,7 @@ __device__ __forceinline__ void append_page(const AppendParams& p, int block) {
 constexpr int kRowBatch = 4;  // heads_per_unit at most, all read before any is written
 __device__ __forceinline__ void append_rows(const AppendParams& p, int block) {
     const int runs = (p.row_heads + 4 * p.heads_per_unit - 1) / (4 * p.heads_per_unit);
-    const long long unit = static_cast<long long>(block) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const long long unit = static_cast<long long>(block) * (kAppendThreads / 32) + (threadIdx.x >> 5);
     const long long tok = unit / runs;
     if (tok >= p.total) return;
     const int t = static_cast<int>(tok), run = static_cast<int>(unit % runs);
@@ -422,10 +442,7 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int block) {
     }
 }
 
-// Three CTAs of 256 threads on an SM: with fewer the loads in flight do not
-// cover the memory's latency, with four the rows spill (measured: 46.8 / 40.2 /
-// 43.6 us for 229 MB of ragged prompts with two, three, four).
-__global__ void __launch_bounds__(256, 3)
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtasPerSm)
     attn_cache_append_kernel(const __grid_constant__ AppendParams p) {
     // All that came before on the stream is done and visible from here on.
     asm volatile("griddepcontrol.wait;" ::: "memory");
