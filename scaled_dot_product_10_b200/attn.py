@@ -661,7 +661,7 @@ def attn_fwd_cache(q, cache: KVCache, page_table, seqlens_k, cu_seqlens_q=None,
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if max_seqlen_q is None:
-        max_seqlen_q = total_q if cu_seqlens_q is not None else -(-total_q // batch)
+        max_seqlen_q = total_q if cu_seqlens_q is not None else -(-total_q // max(batch, 1))
     with _on_device(dev):
         o, lse = _outputs(q, o, lse, (total_q, h_q, d), (h_q, total_q), stream)
         if total_q == 0:

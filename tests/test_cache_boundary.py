@@ -281,3 +281,14 @@ def test_fwd_refuses(lib, changes):
     with pytest.raises((ValueError, TypeError)):
         attn.attn_fwd_cache(args.pop("q"), attn.KVCache(*pool()), **args)
     assert all(name == "attn_fwd_cache_workspace_bytes" for name, _ in lib.calls)
+
+
+def test_an_empty_batch_launches_nothing(lib):
+    cache = attn.KVCache(*pool())
+    t, sl = FakeCuda(torch.zeros(0, 4, dtype=torch.int32)), i32()
+    o, lse = bf16(0, 4, 128), f32(4, 0)
+    assert attn.attn_fwd_cache(bf16(0, 4, 128), cache, t, sl, o=o, lse=lse,
+                               stream=STREAM) == (o, lse)
+    assert attn.attn_cache_append(cache, bf16(0, 2, 128), bf16(0, 2, 128), t, sl, q=bf16(0, 4, 128),
+                                  q_out=o, stream=STREAM) is o
+    assert not lib.calls
