@@ -150,8 +150,10 @@ int attn_cache_append(const attn_cache_t* cache, const void* k, const void* v, c
  *
  * A row that sees no key (a sequence of length 0, or a causal one with more
  * new rows than keys) gets O = 0 and LSE = -inf.  What lies in a page past the
- * sequence's end is never used, whatever its bits.  Keys past
- * max_pages * page_size are not there.
+ * sequence's end is never used, whatever its bits, nor what lies before the
+ * window of the sequence's first query.  A NaN or infinity that a row sees
+ * reaches its result, and may reach other rows of the same sequence and call.
+ * Keys past max_pages * page_size are not there.
  *
  * Numerics: BF16 pages as attn_fwd (P rounded to BF16).  E4M3 pages go to the
  * tensor core as they are; a query is the sum of two E4M3 numbers (exact for
@@ -163,7 +165,8 @@ int attn_cache_append(const attn_cache_t* cache, const void* k, const void* v, c
  *
  * Two launches, or one where the rows of page_table hold at most 512 keys
  * (attn_last_launch_count tells).  Errors as attn_cache_append, plus ATTN_ERR_INVALID for a
- * non-finite scale, a window without causal and a workspace too small.
+ * non-finite scale, a window without causal, max_pages * page_size above
+ * 2^31 - 256 and a workspace too small.
  */
 int attn_fwd_cache(const attn_cache_t* cache, const void* q, void* o, float* lse,
                    const int* page_table, const int* seqlens_k, const int* cu_seqlens_q,

@@ -102,8 +102,8 @@ bool encode_pool(CUtensorMap* m, const attn_cache_t* c, void* base, int box) {
 // Query rows of a tile: the smallest of 8, 16 and 32 that holds a sequence's
 // rows of one key/value head, else 128 (the wide kernel).  Rows that are
 // not there cost time: with tiles of at least 8, 16, 32 and 128 rows, eight
-// rows of 64 sequences of 8192 E4M3 keys take 38.3, 40.3, 54.1 and 87.9 us, of
-// 16 sequences of 4096 BF16 keys 66.0, 66.7, 71.9 and 72.8 us.
+// rows a head of 64 sequences of 8192 E4M3 keys take 38.3, 40.3, 54.1 and 87.9
+// us, one row a head of 16 sequences of 4096 BF16 keys 66.0, 66.7, 71.9 and 72.8.
 int cache_rows(int group, int max_seqlen) {
     const long long rows = static_cast<long long>(group) * max_seqlen;
     return rows <= 8 ? 8 : (rows <= 16 ? 16 : (rows <= 32 ? 32 : 128));
@@ -249,7 +249,7 @@ extern "C" int attn_cache_append(const attn_cache_t* c, const void* k, const voi
     // Row role: a warp takes four heads of a token, and up to 16 (which share
     // its angles) while every SM still gets a warp.  Four always: 79.5 us (BF16
     // prompts of 2048) and 102 us (32768 tokens) against 40.4 and 61.0; 256
-    // tokens of 32 heads take 4.7 us with 16 heads a warp, 5.4 with eight.
+    // tokens of 16 heads take 4.7 us with 16 heads a warp, 5.4 with four.
     p.heads_per_unit = 1;
     while (p.heads_per_unit < cache::kRowBatch && p.heads_per_unit * 4 < p.row_heads &&
            static_cast<long long>(total) * p.row_heads / (8 * p.heads_per_unit) >= kRowWarps)
@@ -317,7 +317,8 @@ extern "C" int attn_fwd_cache(const attn_cache_t* c, const void* q, void* o, flo
     p.head_tiles = (p.group + p.heads_per_tile - 1) / p.heads_per_tile;
     // The share of a CTA has a 32-bit number of units (row tiles x key tiles).
     const long long cap = static_cast<long long>(max_pages) * c->page_size;
-    const long long key_tiles = std::min(cap, kMaxInt) / 128 + 1;
+    if (cap > kMaxInt - 255) return ATTN_ERR_INVALID;  // tiles' ends are 32-bit keys
+    const long long key_tiles = cap / 128 + 1;
     const long long row_tiles =
         (cu_seqlens_q ? std::min(static_cast<long long>(total_q) / p.q_per_tile + batch,
                                  static_cast<long long>(batch) *

@@ -763,9 +763,10 @@ __device__ __forceinline__ void store_weights(const float (&w)[Shape<kE, kR>::kS
     }
 }
 
-// Four warps: thread r holds key r of the tile, and Tensor Memory lane r.  A wait that gives up sets `dead`: the warp then goes through
-// its tiles without waiting (it keeps the group's barriers in step) and the
-// results are unspecified.
+// Four warps: thread r holds key r of the tile, and Tensor Memory lane r.  A
+// wait that gives up sets `dead`: the warp then goes through its tiles without
+// waiting (it keeps the group's barriers in step) and the results are
+// unspecified.
 template <bool kE, int kR>
 __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, uint8_t* sq,
                                              uint32_t sp, uint8_t* ring, uint32_t tmem,
@@ -946,12 +947,12 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
                 store_weights<kE, kR>(x, p_row, r & 7, b * kSub);
             }
             if (kCols > kSub) scores_read();
-            if (key0 + 127 >= it.r.end) {
-                // Slots past the end hold anything: zero them before 0 * NaN.
+            if (key0 + 127 >= it.r.end || key0 < it.r.beg) {
+                // Slots that no row sees hold anything: zero them before 0 * NaN.
                 // V's tile in the ring: K0, then K(j+1), V(j) in turn.
                 const uint32_t v_used = used + (j + 1 < it.m ? 2 * j + 2 : 2 * it.m - 1);
                 wait(&tl.full[v_used % S::kSlots], (v_used / S::kSlots) & 1);
-                if (key >= it.r.end) {
+                if (key >= it.r.end || key < it.r.beg) {
                     uint4* row = reinterpret_cast<uint4*>(ring + (v_used % S::kSlots) * S::kTile +
                                                           r * 128);
 #pragma unroll
@@ -996,10 +997,10 @@ __device__ __forceinline__ void softmax_role(const FwdCacheParams& p, Tail& tl, 
                 if (row >= 0) {
                     const int q = row / p.h_q;
                     p.lse[static_cast<long long>(row - q * p.h_q) * p.total_q + q] =
-                        sum > 0.f ? (log2f(sum) - rows.offset[col]) * 0.69314718055994531f
+                        sum != 0.f ? (log2f(sum) - rows.offset[col]) * 0.69314718055994531f
                                   : -CUDART_INF_F;
                 }
-                tl.alpha[col] = sum > 0.f ? 1.f / sum : 0.f;
+                tl.alpha[col] = sum != 0.f ? 1.f / sum : 0.f;
             } else {
                 p.part_ml[slot * kR + col] = make_float2(-rows.offset[col], sum);
             }
@@ -1120,8 +1121,9 @@ __global__ void __launch_bounds__(Shape<kE, kR>::kThreads, Shape<kE, kR>::kCtasP
 // The parts of the items that a share's border cuts:
 //     O = sum_i 2^(u_i - U) acc_i / sum_i 2^(u_i - U) l_i,   U = max u_i.
 // Blocks (c, y): the item that begins in share c and goes on in the next ones.
-// With at most kMergeWarps parts a warp takes a row at a time; with more (long keys, few rows) a block takes rows y, y + 8, ... and a
-// warp every eighth part, and the warps' sums are joined in order.
+// With at most kMergeWarps parts a warp takes a row at a time; with more (long
+// keys, few rows) a block takes rows y, y + 8, ... and a warp every eighth part,
+// and the warps' sums are joined in order.
 constexpr int kMergeWarps = 8;
 constexpr int kMergeParts = 8;  // parts whose loads are in flight together
 
@@ -1151,7 +1153,7 @@ __device__ __forceinline__ Merged merge_parts(const float2* ml, const float4* o,
         float u = r.u;
 #pragma unroll
         for (int k = 0; k < kMergeParts; ++k) {
-            if (i0 + k * step >= parts || !(m[k].y > 0.f)) m[k] = make_float2(-CUDART_INF_F, 0.f);
+            if (i0 + k * step >= parts || m[k].y == 0.f) m[k] = make_float2(-CUDART_INF_F, 0.f);
             u = fmaxf(u, m[k].x);
         }
         const float ref = u > -CUDART_INF_F ? u : 0.f;
@@ -1164,7 +1166,7 @@ __device__ __forceinline__ Merged merge_parts(const float2* ml, const float4* o,
 #pragma unroll
         for (int k = 0; k < kMergeParts; ++k) {
             const float a = exp2f(m[k].x - ref);
-            if (a > 0.f) {
+            if (a != 0.f) {  // (a NaN counts)
                 r.l = fmaf(a, m[k].y, r.l);
                 r.acc.x = fmaf(a, x[k].x, r.acc.x);
                 r.acc.y = fmaf(a, x[k].y, r.acc.y);
@@ -1188,14 +1190,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     auto write = [&](int c, const Merged& m) {
         const int qi = p.div_heads.div(c), e = c - qi * p.heads_per_tile;
-        const float inv = m.l > 0.f ? 1.f / m.l : 0.f;
+        const float inv = m.l != 0.f ? 1.f / m.l : 0.f;
         const int q = meta.y + qi, h = meta.z + e;
         reinterpret_cast<uint2*>(p.o + (static_cast<long long>(q) * p.h_q + h) * kHeadDim)[lane] =
             make_uint2(ptx::pack_bf16x2(m.acc.x * inv, m.acc.y * inv),
                        ptx::pack_bf16x2(m.acc.z * inv, m.acc.w * inv));
         if (lane == 0)
             p.lse[static_cast<long long>(h) * p.total_q + q] =
-                m.l > 0.f ? (log2f(m.l) + m.u) * 0.69314718055994531f : -CUDART_INF_F;
+                m.l != 0.f ? (log2f(m.l) + m.u) * 0.69314718055994531f : -CUDART_INF_F;
     };
     auto there = [&](int c) -> bool {
         const int qi = p.div_heads.div(c), e = c - qi * p.heads_per_tile;

@@ -377,11 +377,11 @@ __device__ __forceinline__ void wide_softmax_role(const FwdCacheParams& p, WideT
                 }
                 ptx::tmem_wait_st();
             }
-            if (key0 + 127 >= it.r.end) {
-                // Slots past the end hold anything: zero them before 0 * NaN.
+            if (key0 + 127 >= it.r.end || key0 < it.r.beg) {
+                // Slots that no row sees hold anything: zero them before 0 * NaN.
                 const uint32_t v_used = used + (j + 1 < it.m ? 2 * j + 2 : 2 * it.m - 1);
                 wait(&tl.full[v_used % S::kSlots], (v_used / S::kSlots) & 1);
-                if (key0 + row >= it.r.end && (!kE || side == 0)) {
+                if ((key0 + row >= it.r.end || key0 + row < it.r.beg) && (!kE || side == 0)) {
                     uint4* at = reinterpret_cast<uint4*>(ring + (v_used % S::kSlots) * S::kTile +
                                                          side * 16384 + row * 128);
 #pragma unroll
@@ -412,14 +412,14 @@ __device__ __forceinline__ void wide_softmax_role(const FwdCacheParams& p, WideT
         wait(&tl.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
         ptx::tc_fence_after();
         if (active) {
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            const float inv = sum != 0.f ? 1.f / sum : 0.f;
             if (side == 0) {
                 if (!whole) {
                     p.part_ml[slot * 128 + row] = make_float2(-offset, sum);
                 } else if (view.row >= 0) {
                     const int q = view.row / p.h_q;
                     p.lse[static_cast<long long>(view.row - q * p.h_q) * p.total_q + q] =
-                        sum > 0.f ? (log2f(sum) - offset) * 0.69314718055994531f : -CUDART_INF_F;
+                        sum != 0.f ? (log2f(sum) - offset) * 0.69314718055994531f : -CUDART_INF_F;
                 }
             }
 #pragma unroll

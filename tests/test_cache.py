@@ -239,6 +239,58 @@ def test_page_numbers_outside_the_pool(kind):
     run_attend(Pool([112], 16, 1, kind, seed=6), [5000], [1], 4, causal=False)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("news,h_q", [([1, 1], 8), ([5, 2], 8), ([1, 1], 128), ([130, 7], 8)])
+@pytest.mark.parametrize("window", [0, 50, 200])
+def test_slots_before_the_window_hold_anything(kind, news, h_q, window):
+    """A server hands pages before the window to others: NaN there, in keys,
+    values and the scales of whole pages, changes nothing."""
+    lens = [900, 333]
+    pool = Pool(lens, 16, 2, kind, seed=window + h_q)
+    for b, (length, n) in enumerate(zip(lens, news)):
+        first = length - n - window
+        for j in range(-(-first // 16)):
+            pid, last = int(pool.table[b, j]), min(first - 16 * j, 16)
+            for x in pool.d_pages:
+                bits = torch.uint8 if kind == "e4m3" else torch.int16
+                x.view(bits)[pid, :last] = NAN8 if kind == "e4m3" else NAN16
+            if kind == "e4m3" and last == 16:
+                for x in pool.d_scale:
+                    x[pid] = float("nan")
+    run_attend(pool, lens, news, h_q, window=window)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,h_q", [([300, 200], 8), ([300, 200], 128), ([9000, 1200], 8),
+                                      ([9000, 1200], 128)])
+def test_nan_in_a_seen_key_reaches_the_rows(kind, lens, h_q):
+    """Short tables and shares that are joined, few rows and many."""
+    pool = Pool(lens, 16, 2, kind, seed=h_q)
+    clean = run_attend(pool, lens, [1, 1], h_q)[1:]
+    bits, nan = (torch.uint8, NAN8) if kind == "e4m3" else (torch.int16, NAN16)
+    at = (int(pool.table[0, 10]), 3, 1)
+    seen = slice(h_q // 2, h_q)  # the query heads of key/value head 1
+
+    def run():
+        q = torch.randn(2, h_q, 128, generator=torch.Generator().manual_seed(5))
+        cu = torch.tensor([0, 1, 2], dtype=torch.int32).cuda()
+        return attn.attn_fwd_cache(q.to(torch.bfloat16).cuda(), pool.cache, pool.d_table,
+                                   torch.tensor(lens, dtype=torch.int32).cuda(), cu_seqlens_q=cu,
+                                   max_seqlen_q=1)
+    for t, dims in ((0, slice(0, 128)), (1, slice(7, 8))):
+        keep = pool.d_pages[t][at].clone()
+        pool.d_pages[t].view(bits)[at][7] = nan
+        o, lse = run()
+        pool.d_pages[t][at] = keep
+        assert attn.attn_status() == attn.ATTN_OK
+        assert bool(o[0, seen, dims].isnan().all())
+        assert bool(lse[seen, 0].isnan().all()) == (t == 0)
+        o[0, seen, dims] = clean[0][0, seen, dims]
+        if t == 0:
+            lse[seen, 0] = clean[1][seen, 0]
+        assert torch.equal(o, clean[0]) and torch.equal(lse, clean[1])
+
+
 def test_strided_queries_stream_and_graph():
     lens = [400, 90, 33]
     pool = Pool(lens, 16, 2, "e4m3", seed=9)

@@ -80,6 +80,7 @@ FWD_RULES = [
     (dict(window_left=4, causal=0), attn.ATTN_ERR_INVALID),
     (dict(q_stride=500), attn.ATTN_ERR_INVALID),
     (dict(total_q=1 << 30, max_seqlen_q=1 << 30), attn.ATTN_ERR_INVALID),  # 32-bit row numbers
+    (dict(max_pages=1 << 27), attn.ATTN_ERR_INVALID),  # 2^31 keys of pages of 16
     (dict(q=A + 4), attn.ATTN_ERR_ALIGN), (dict(o=A + 8), attn.ATTN_ERR_ALIGN),
     (dict(lse=A + 2), attn.ATTN_ERR_ALIGN), (dict(workspace=A + 16), attn.ATTN_ERR_ALIGN),
 ]

@@ -31,9 +31,9 @@ class Barrier:
 class Model:
     """kind: "narrow" or "wide"; warps: softmax warps of a tile."""
 
-    def __init__(self, rng, kind, items, slots, warps, p_bars):
+    def __init__(self, rng, kind, items, slots, warps, p_bars, zeroed=False):
         self.rng, self.kind, self.items, self.slots, self.warps = rng, kind, items, slots, warps
-        self.p_bars = p_bars
+        self.p_bars, self.zeroed = p_bars, zeroed
         self.bufs = 3 if kind == "wide" else 2
         self.full = [Barrier(1) for _ in range(slots)]
         self.empty = [Barrier(1) for _ in range(slots)]
@@ -120,7 +120,7 @@ class Model:
                 yield from weigh()
 
     def softmax(self, warp):
-        g = 0
+        g = used = 0
         self.q_item[warp] = 0
         self.q_full.arrive()
         yield
@@ -148,9 +148,16 @@ class Model:
                 else:
                     self.p_tile[b][warp] = g
                 yield
+                if self.zeroed and j in (0, m - 1):
+                    # slots of V that no row sees are zeroed: it must be there
+                    v = used + (2 * j + 2 if j + 1 < m else 2 * m - 1)
+                    while not self.full[v % self.slots].passed((v // self.slots) & 1):
+                        yield
+                    assert self.ring[v % self.slots] == ("V", g), "another tile's V"
                 self.p_full[g % len(self.p_full)].arrive()
                 g += 1
                 yield
+            used += 2 * m
             if item + 1 < len(self.items):
                 self.q_item[warp] = item + 1
                 # no warp goes on before all have staged their rows
@@ -233,6 +240,14 @@ def test_narrow(seed):
 def test_wide(seed):
     rng = random.Random(1000 + seed)
     Model(rng, "wide", items_of(rng), rng.choice([5, 8]), 3, 2).run()
+
+
+@pytest.mark.parametrize("kind,slots,warps,p_bars", [("narrow", [3, 5, 6], 4, 1),
+                                                     ("wide", [5, 8], 3, 2)])
+@pytest.mark.parametrize("seed", range(40))
+def test_values_zeroed_at_both_ends(seed, kind, slots, warps, p_bars):
+    rng = random.Random(3000 + seed)
+    Model(rng, kind, items_of(rng), rng.choice(slots), warps, p_bars, zeroed=True).run()
 
 
 def test_one_barrier_for_wide_weights_is_caught():
